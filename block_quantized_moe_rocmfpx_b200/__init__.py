@@ -80,7 +80,16 @@ _debug_fault = _proto("rfx_debug_set_fault", _i32, [_i32, ctypes.c_longlong])
 _prefill = _proto("moe_ffn_prefill", _i32, [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _vp])
 _pf_ws_bytes_ex = _proto("moe_prefill_workspace_bytes_ex", _sz, [_vp, _i32, _i32])
 _prefill_ex = _proto("moe_ffn_prefill_ex", _i32, [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _i32, _vp])
+_group_ws = _proto("moe_group_workspace_bytes", _sz, [_i32, _i32, _i32])
+_group = _proto("moe_group_tokens", _i32,
+                [_vp, _i32, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
+_group_bwd = _proto("moe_group_tokens_backward", _i32, [_vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp])
+_combine = _proto("moe_combine_rows", _i32, [_vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _vp])
+_combine_bwd = _proto("moe_combine_rows_backward", _i32,
+                      [_vp, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp])
+_router_bwd = _proto("moe_router_topk_backward", _i32, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp])
 RFX_PREFILL_BF16, RFX_PREFILL_EXACT = 0, 1
+RFX_BF16, RFX_F32, RFX_F16 = 0, 1, 2
 
 
 class moe_prefill_ws_view(ctypes.Structure):
@@ -95,7 +104,9 @@ EXPORTED = ["rfx_last_error", "rfx_packed_bytes", "rfx_pack", "rfx_unpack", "rfx
             "rfx_ws_status", "moe_ffn_forward", "moe_ffn_forward_logits", "moe_ffn_forward_static", "moe_rms_norm_bf16",
             "moe_stack_workspace_bytes", "moe_stack_forward", "moe_prefill_workspace_bytes", "moe_ffn_prefill",
             "moe_prefill_workspace_bytes_ex", "moe_ffn_prefill_ex",
-            "moe_prefill_view", "moe_router_logits", "moe_router_project_topk",
+            "moe_prefill_view", "moe_router_logits", "moe_router_project_topk", "moe_router_topk_backward",
+            "moe_group_workspace_bytes", "moe_group_tokens", "moe_group_tokens_backward", "moe_combine_rows",
+            "moe_combine_rows_backward",
             "moe_ffn_host_scratch_bytes", "moe_ffn_forward_host", "rfx_debug_set_fault"]
 
 
@@ -184,6 +195,120 @@ def moe_router_project_topk(w_router, bias, x, k: int, logits, idx, w, stream=No
     T = x.shape[0]
     _check(_router_proj_topk(_ptr(w_router), _ptr(bias), _ptr(x), T, H, E, k, _ptr(logits), _ptr(idx), _ptr(w),
                              _stream(stream)))
+
+
+def _dtype_codes():
+    import torch
+    return {torch.bfloat16: RFX_BF16, torch.float32: RFX_F32, torch.float16: RFX_F16}
+
+
+_DTYPES = None
+
+
+def _rows_dtype(t) -> int:
+    """rfx_dtype of a tensor's elements."""
+    global _DTYPES
+    if _DTYPES is None:
+        _DTYPES = _dtype_codes()
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"dtype {t.dtype}: bfloat16, float16 or float32 expected")
+    return code
+
+
+def _dense(name: str, t, shape, dtype=None):
+    """Check a tensor of a row or 4-bit call: on the current CUDA device, contiguous,
+    of this shape and type (the C call sees only its pointer)."""
+    import torch
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: must be on the current CUDA device, not {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def moe_router_topk_backward(idx, w, dw, dlogits, stream=None):
+    """dlogits fp32 [T][E] from dw fp32 [T][k], the gradient of moe_router_topk's w
+    (idx int32 / w fp32 [T][k] as it wrote them)."""
+    import torch
+    T, E = dlogits.shape
+    k = idx.shape[-1]
+    _dense("dlogits", dlogits, (T, E), torch.float32)
+    _dense("idx", idx, (T, k), torch.int32)
+    _dense("w", w, (T, k), torch.float32)
+    _dense("dw", dw, (T, k), torch.float32)
+    _check(_router_bwd(_ptr(idx), _ptr(w), _ptr(dw), T, E, k, _ptr(dlogits), _stream(stream)))
+
+
+def moe_group_workspace_bytes(T: int, k: int, E: int) -> int:
+    return int(_group_ws(T, k, E))
+
+
+def moe_group_tokens(x, idx, E: int, xs, pos, rows, offsets, ws, stream=None):
+    """Rows of x [T][H] sorted by expert: xs [T*k][H], pos int32 [T][k], rows int32
+    [T*k], offsets int32 [E+1] from idx int32 [T][k] (device tensors; x and xs may
+    both be None).  ws: moe_group_workspace_bytes(T, k, E) bytes, rfx_ws_init once."""
+    import torch
+    T, k = idx.shape
+    _dense("idx", idx, (T, k), torch.int32)
+    _dense("pos", pos, (T, k), torch.int32)
+    _dense("rows", rows, (T * k,), torch.int32)
+    _dense("offsets", offsets, (E + 1,), torch.int32)
+    if (x is None) != (xs is None):
+        raise ValueError("x and xs: both or neither")
+    H, dt = 1, RFX_F32
+    if x is not None:
+        H, dt = x.shape[-1], _rows_dtype(x)
+        _dense("x", x, (T, H))
+        _dense("xs", xs, (T * k, H), x.dtype)
+    _check(_group(_ptr(x), dt, T, H, _ptr(idx), k, E, _ptr(xs), _ptr(pos), _ptr(rows), _ptr(offsets), _ptr(ws),
+                  ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_group_tokens_backward(dxs, pos, dx, stream=None):
+    """dx [T][H] = sum over j of dxs[pos[t][j]] (dxs [T*k][H] of dx's type, pos int32 [T][k])."""
+    import torch
+    T, k = pos.shape
+    H = dx.shape[-1]
+    _dense("pos", pos, (T, k), torch.int32)
+    _dense("dxs", dxs, (T * k, H), dx.dtype)
+    _dense("dx", dx, (T, H))
+    _check(_group_bwd(_ptr(dxs), _rows_dtype(dx), T, H, _ptr(pos), k, _ptr(dx), _stream(stream)))
+
+
+def moe_combine_rows(ys, pos, w, y, base=None, stream=None):
+    """y [T][H] = base + sum over j of w[t][j] * ys[pos[t][j]] (ys [T*k][H], pos int32
+    and w fp32 [T][k]; y and base of ys's type or fp32)."""
+    import torch
+    T, k = pos.shape
+    H = y.shape[-1]
+    _dense("pos", pos, (T, k), torch.int32)
+    _dense("w", w, (T, k), torch.float32)
+    _dense("ys", ys, (T * k, H))
+    _dense("y", y, (T, H))
+    if base is not None:
+        _dense("base", base, (T, H), y.dtype)
+    _check(_combine(_ptr(ys), _rows_dtype(ys), T, H, _ptr(pos), k, _ptr(w), _ptr(base), _ptr(y), _rows_dtype(y),
+                    _stream(stream)))
+
+
+def moe_combine_rows_backward(dy, ys, pos, w, dys, dw, stream=None):
+    """dys [T*k][H] and dw fp32 [T][k], the gradients of moe_combine_rows from dy [T][H]
+    (of ys's type or fp32)."""
+    import torch
+    T, k = pos.shape
+    H = dy.shape[-1]
+    _dense("pos", pos, (T, k), torch.int32)
+    _dense("w", w, (T, k), torch.float32)
+    _dense("ys", ys, (T * k, H))
+    _dense("dys", dys, (T * k, H), ys.dtype)
+    _dense("dy", dy, (T, H))
+    _dense("dw", dw, (T, k), torch.float32)
+    _check(_combine_bwd(_ptr(dy), _rows_dtype(dy), _ptr(ys), _rows_dtype(ys), T, H, _ptr(pos), k, _ptr(w), _ptr(dys),
+                        _ptr(dw), _stream(stream)))
 
 
 def rfx_gemv_q(fmt: int, W, N: int, K: int, x, y, stream=None):

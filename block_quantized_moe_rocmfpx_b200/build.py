@@ -34,7 +34,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return SO
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = SO + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, "-shared", "-o", tmp, *sources(), "-lgomp"]
+    cmd = [nvcc, *NVCC_FLAGS, "--threads", "0", "-shared", "-o", tmp, *sources(), "-lgomp"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)

@@ -33,4 +33,37 @@ class SmemLimit {
     std::mutex mu_;
 };
 
+// SM count of the current device, queried once per device.
+inline cudaError_t device_sms(int& sms) {
+    static std::atomic<int> cache[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool cached = dev >= 0 && dev < 64;
+    if (cached && (sms = cache[dev].load(std::memory_order_relaxed)) != 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && cached) cache[dev].store(sms, std::memory_order_relaxed);
+    return e;
+}
+
+// Launch as a programmatic dependent of the kernel before it on the stream:
+// the launch overlaps that kernel's tail, and the kernel itself waits
+// (grid_dep_wait) before its first access to global memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                             Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    (void)cudaGetLastError();   // an earlier call's launch error is not this launch's
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace rfx

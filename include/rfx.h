@@ -101,6 +101,9 @@ typedef enum {
 
 typedef enum { RFX_FP2 = 2, RFX_FP3 = 3, RFX_FP4 = 4 } rfx_format;
 
+/* Element types of the calls that take more than one. */
+typedef enum { RFX_BF16 = 0, RFX_F32 = 1, RFX_F16 = 2 } rfx_dtype;
+
 /* Thread-local text of the last non-OK status returned on this thread. */
 const char* rfx_last_error(void);
 
@@ -174,6 +177,83 @@ int moe_router_logits(const void* w_router, const float* bias, const void* x, in
  */
 int moe_router_project_topk(const void* w_router, const float* bias, const void* x, int T, int H, int E, int k,
                             float* logits, int32_t* idx, float* w, void* stream);
+
+/*
+ * Gradient of moe_router_topk's weights: with w the softmax over the k
+ * selected logits and dw the gradient of w,
+ *   dlogits[t][idx[t][j]] = w[t][j] * (dw[t][j] - sum_i w[t][i] * dw[t][i]),
+ * and 0 for the logits that were not selected (the selection itself has no
+ * gradient).  idx, w: device, as moe_router_topk wrote them; an id that appears
+ * twice in a row receives the sum of its entries, an id outside [0, E)
+ * nothing.  dw: device fp32 [T][k].  dlogits: device fp32 [T][E], written
+ * whole.  fp32 arithmetic in a fixed order.  Limits as moe_router_topk.
+ */
+int moe_router_topk_backward(const int32_t* idx, const float* w, const float* dw, int T, int E, int k, float* dlogits,
+                             void* stream);
+
+/* ------------------------------------------- rows grouped by expert ----- */
+
+/*
+ * Token rows sorted by expert, for experts that run outside moe_ffn_forward
+ * (another weight form, a product of the caller's own), and the way back.
+ * Entry i = t * k + j routes token t to expert idx[t][j].  The entries sorted by
+ * (expert, i) are the grouped rows; R = T * k rows at most:
+ *   pos[t][j]    the row of the entry, or -1 if it has none
+ *   rows[r]      the entry t * k + j of row r, r < offsets[E]
+ *   offsets[e]   first row of expert e; offsets[E] = rows in use
+ *   xs[r]        x[rows[r] / k]
+ * (the order of moe_ffn_prefill's grouping).  An id of -1 marks an entry without an
+ * expert (a padded token): it gets no row.  Any other id outside [0, E) gets
+ * no row either and sets the workspace's device error flag
+ * (rfx_ws_status: RFX_EDEVICE).  An id repeated in a token makes two rows.
+ * Entries of rows and rows of xs from offsets[E] on are left as they were.
+ * x: device [T][H] of dtype; xs: device [T * k][H]; x and xs may both be NULL
+ * (the places only).  idx: device int32 [T][k].  pos, rows, offsets: device
+ * int32 [T][k], [T * k], [E + 1].  ws: device, 256-byte aligned,
+ * moe_group_workspace_bytes(T, k, E) bytes, zeroed once with rfx_ws_init; calls
+ * that overlap on the GPU must use different workspaces.  One launch, or two for
+ * longer batches; no atomics on global memory, so the result is the same every time.
+ * Limits: T >= 0, H >= 1, 1 <= E <= 1024, 1 <= k <= 16 (k may exceed E),
+ * T * k < 2^31.  T = 0 is a no-op (offsets are not written).  Rows that are a
+ * multiple of 16 bytes at 16-byte aligned pointers are copied fastest; any H is accepted.
+ */
+size_t moe_group_workspace_bytes(int T, int k, int E);
+int moe_group_tokens(const void* x, rfx_dtype dtype, int T, int H, const int32_t* idx, int k, int E, void* xs,
+                     int32_t* pos, int32_t* rows, int32_t* offsets, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of moe_group_tokens with respect to x: dx[t] = sum_j dxs[pos[t][j]],
+ * j ascending, summed in fp32 and rounded once to dtype.  An entry of pos
+ * outside [0, T * k) contributes nothing.  dxs: device [T * k][H]; dx: device
+ * [T][H], both of dtype.
+ */
+int moe_group_tokens_backward(const void* dxs, rfx_dtype dtype, int T, int H, const int32_t* pos, int k, void* dx,
+                              void* stream);
+
+/*
+ * The way back with the router's weights (the combine of moe_ffn_forward over
+ * rows of the caller's own):
+ *   y[t] = base[t] + sum_j w[t][j] * ys[pos[t][j]]
+ * j ascending, summed in fp32, base added last, rounded once to y_dtype.  An entry of pos
+ * outside [0, T * k) contributes nothing (its w is not read into the sum).
+ * ys: device [T * k][H] of dtype; w: device fp32 [T][k]; base: device [T][H] of
+ * y_dtype (the shared expert's output, a residual) or NULL; y: device [T][H] of
+ * y_dtype, which is dtype or fp32; y may be base, but may not overlap ys.  One launch.
+ */
+int moe_combine_rows(const void* ys, rfx_dtype dtype, int T, int H, const int32_t* pos, int k, const float* w,
+                     const void* base, void* y, rfx_dtype y_dtype, void* stream);
+
+/*
+ * Gradients of moe_combine_rows (that of base is dy itself):
+ *   dys[pos[t][j]] = w[t][j] * dy[t]          (rounded once to dtype)
+ *   dw[t][j]       = sum_h dy[t][h] * ys[pos[t][j]][h]
+ * fp32 sums in a fixed order.  Where pos has no row, dw is 0; rows of dys that no
+ * entry names are left as they were.  dy: device [T][H] of y_dtype; ys and dys:
+ * device [T * k][H] of dtype (dys may be ys); dw: device fp32 [T][k].  pos must not name a
+ * row twice.  One launch.
+ */
+int moe_combine_rows_backward(const void* dy, rfx_dtype y_dtype, const void* ys, rfx_dtype dtype, int T, int H,
+                              const int32_t* pos, int k, const float* w, void* dys, float* dw, void* stream);
 
 /* --------------------------------------------------------------- GEMV --- */
 

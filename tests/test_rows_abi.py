@@ -1,0 +1,87 @@
+"""Argument checks of the row operators: every refusal is made before any CUDA
+call, so the tests run without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import block_quantized_moe_rocmfpx_b200 as rfx
+
+A = 4096          # a made-up aligned address; no refused call reads it
+
+
+def code(rc):
+    if rc != rfx.RFX_OK:
+        assert rfx.rfx_last_error()
+    return rc
+
+
+def group(x=A, dt=0, T=4, H=8, idx=A, k=2, E=4, xs=A, pos=A, rows=A, off=A, ws=A, n=1 << 20):
+    return code(rfx._group(x, dt, T, H, idx, k, E, xs, pos, rows, off, ws, n, None))
+
+
+def test_group_refusals():
+    E = rfx.RFX_EINVAL
+    for bad in ({"dt": 3}, {"dt": -1}, {"T": -1}, {"H": 0}, {"k": 0}, {"k": 17}, {"E": 0}, {"E": 1025}, {"idx": None},
+                {"pos": None}, {"rows": None}, {"off": None}, {"ws": None}, {"x": None}, {"xs": None},
+                {"x": A + 1}, {"xs": A + 1}, {"dt": 1, "x": A + 2}, {"ws": A + 16}, {"n": 255}):
+        assert group(**bad) == E, bad
+    assert group(T=2 ** 30, k=16) == rfx.RFX_EUNSUPPORTED
+    assert group(T=0, idx=None, ws=None) == rfx.RFX_OK
+
+
+def test_group_workspace_bytes():
+    assert rfx.moe_group_workspace_bytes(4, 6, 256) == 256
+    assert rfx.moe_group_workspace_bytes(8192, 6, 256) > 256
+    for T, k, E in ((0, 1, 1), (1, 0, 1), (1, 17, 1), (1, 1, 0), (1, 1, 1025), (2 ** 30, 16, 4)):
+        assert rfx.moe_group_workspace_bytes(T, k, E) == 0
+
+
+def test_group_backward_refusals():
+    def call(dxs=A, dt=0, T=4, H=8, pos=A, k=2, dx=A):
+        return code(rfx._group_bwd(dxs, dt, T, H, pos, k, dx, None))
+    for bad in ({"dt": 5}, {"T": -1}, {"H": 0}, {"k": 0}, {"k": 17}, {"dxs": None}, {"pos": None}, {"dx": None},
+                {"dxs": A + 1}, {"dx": A + 1}):
+        assert call(**bad) == rfx.RFX_EINVAL, bad
+    assert call(T=0, dx=None) == rfx.RFX_OK
+
+
+def test_combine_refusals():
+    def call(ys=A, dt=0, T=4, H=8, pos=A, k=2, w=A, base=None, y=A, yd=1):
+        return code(rfx._combine(ys, dt, T, H, pos, k, w, base, y, yd, None))
+    for bad in ({"dt": 5}, {"yd": 2}, {"dt": 1, "yd": 0}, {"yd": 7}, {"T": -1}, {"H": 0}, {"k": 0}, {"k": 17},
+                {"ys": None}, {"pos": None}, {"w": None}, {"y": None}, {"ys": A + 1}, {"y": A + 2}, {"base": A + 2}):
+        assert call(**bad) == rfx.RFX_EINVAL, bad
+    assert call(T=0, y=None) == rfx.RFX_OK
+    assert call(T=2 ** 27, H=2 ** 13, k=1) == rfx.RFX_EUNSUPPORTED
+
+
+def test_combine_backward_refusals():
+    def call(dy=A, yd=1, ys=A, dt=0, T=4, H=8, pos=A, k=2, w=A, dys=A, dw=A):
+        return code(rfx._combine_bwd(dy, yd, ys, dt, T, H, pos, k, w, dys, dw, None))
+    for bad in ({"dt": 5}, {"yd": 2}, {"T": -1}, {"H": 0}, {"k": 17}, {"dy": None}, {"ys": None}, {"pos": None},
+                {"w": None}, {"dys": None}, {"dw": None}, {"dy": A + 2}, {"ys": A + 1}, {"dys": A + 1}):
+        assert call(**bad) == rfx.RFX_EINVAL, bad
+    assert call(T=0, dw=None) == rfx.RFX_OK
+
+
+def test_router_backward_refusals():
+    def call(idx=A, w=A, dw=A, T=4, E=8, k=2, dl=A):
+        return code(rfx._router_bwd(idx, w, dw, T, E, k, dl, None))
+    for bad in ({"T": -1}, {"E": 0}, {"E": 1025}, {"k": 0}, {"k": 9}, {"E": 64, "k": 17}, {"idx": None}, {"w": None},
+                {"dw": None}, {"dl": None}):
+        assert call(**bad) == rfx.RFX_EINVAL, bad
+    assert call(T=0, dl=None) == rfx.RFX_OK
+
+
+def test_python_refuses_host_tensors():
+    t = torch.zeros((2, 2))
+    with pytest.raises(ValueError):
+        rfx.moe_router_topk_backward(t.int(), t, t, torch.zeros((2, 4)))
+    with pytest.raises(ValueError):
+        rfx.moe_combine_rows(torch.zeros((4, 8)), t.int(), t, torch.zeros((2, 8)))
+
+
+def test_dtype_codes_match_the_header():
+    assert (rfx.RFX_BF16, rfx.RFX_F32, rfx.RFX_F16) == (0, 1, 2)
+    assert ctypes.sizeof(ctypes.c_int) == 4
