@@ -88,6 +88,15 @@ _combine = _proto("moe_combine_rows", _i32, [_vp, _i32, _i32, _i32, _vp, _i32, _
 _combine_bwd = _proto("moe_combine_rows_backward", _i32,
                       [_vp, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp])
 _router_bwd = _proto("moe_router_topk_backward", _i32, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp])
+_g4_bytes = _proto("rfx_g4_packed_bytes", _sz, [_i64, _i64, _i32, _i32])
+_g4_pack = _proto("rfx_g4_pack", _i32, [_vp, _vp, _vp, _i64, _i64, _i32, _vp, _sz])
+_g4_unpack = _proto("rfx_g4_unpack", _i32, [_vp, _i64, _i64, _i32, _vp, _vp, _vp])
+_g4_pack_device = _proto("rfx_g4_pack_device", _i32, [_vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp])
+_gemv_g4 = _proto("rfx_gemv_g4", _i32, [_vp, _i64, _i64, _i32, _i32, _vp, _i32, _i32, _vp, _vp])
+_moe_g4 = _proto("moe_gemv_g4", _i32,
+                 [_vp, _sz, _i32, _i64, _i64, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp])
+_moe_gate_up_g4 = _proto("moe_gate_up_g4", _i32,
+                         [_vp, _vp, _sz, _i32, _i64, _i64, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp])
 RFX_PREFILL_BF16, RFX_PREFILL_EXACT = 0, 1
 RFX_BF16, RFX_F32, RFX_F16 = 0, 1, 2
 
@@ -106,7 +115,8 @@ EXPORTED = ["rfx_last_error", "rfx_packed_bytes", "rfx_pack", "rfx_unpack", "rfx
             "moe_prefill_workspace_bytes_ex", "moe_ffn_prefill_ex",
             "moe_prefill_view", "moe_router_logits", "moe_router_project_topk", "moe_router_topk_backward",
             "moe_group_workspace_bytes", "moe_group_tokens", "moe_group_tokens_backward", "moe_combine_rows",
-            "moe_combine_rows_backward",
+            "moe_combine_rows_backward", "rfx_g4_packed_bytes", "rfx_g4_pack", "rfx_g4_unpack", "rfx_g4_pack_device",
+            "rfx_gemv_g4", "moe_gemv_g4", "moe_gate_up_g4",
             "moe_ffn_host_scratch_bytes", "moe_ffn_forward_host", "rfx_debug_set_fault"]
 
 
@@ -317,6 +327,104 @@ def rfx_gemv_q(fmt: int, W, N: int, K: int, x, y, stream=None):
     q = x.shape[0]
     x_is_fp32 = 1 if x.dtype == torch.float32 else 0
     _check(_gemv(fmt, _ptr(W), N, K, _ptr(x), x_is_fp32, q, _ptr(y), _stream(stream)))
+
+
+# ------------------------------------------- 4-bit weights, group scales ---
+
+def rfx_g4_packed_bytes(rows: int, cols: int, group: int, zeros: bool = False) -> int:
+    return int(_g4_bytes(rows, cols, group, 1 if zeros else 0))
+
+
+def rfx_g4_pack(codes: np.ndarray, scales: np.ndarray, group: int, zeros: np.ndarray | None = None) -> np.ndarray:
+    """codes uint8 [rows][cols] (< 16), scales binary16 (float16 or its bits) and zeros
+    uint8 (< 16) or None, both [rows][cols/group] -> packed bytes (host)."""
+    codes = np.ascontiguousarray(codes, dtype=np.uint8)
+    rows, cols = codes.shape
+    scales = np.ascontiguousarray(scales)
+    scales = scales.view(np.uint16) if scales.dtype == np.float16 else np.ascontiguousarray(scales, dtype=np.uint16)
+    nbytes = rfx_g4_packed_bytes(rows, cols, group, zeros is not None)
+    if nbytes and scales.shape != (rows, cols // group):
+        raise ValueError(f"scales: shape {scales.shape}, expected {(rows, cols // group)}")
+    if zeros is not None:
+        zeros = np.ascontiguousarray(zeros, dtype=np.uint8)
+        if zeros.shape != scales.shape:
+            raise ValueError(f"zeros: shape {zeros.shape}, expected {scales.shape}")
+    out = np.empty(nbytes, dtype=np.uint8)
+    _check(_g4_pack(_ptr(codes), _ptr(scales), _ptr(zeros), rows, cols, group, _ptr(out), out.nbytes))
+    return out
+
+
+def rfx_g4_unpack(packed: np.ndarray, rows: int, cols: int, group: int, zeros: bool = False):
+    """(codes, scale bits, zeros or None) of rfx_g4_pack's bytes."""
+    packed = np.ascontiguousarray(packed, dtype=np.uint8)
+    if packed.nbytes < rfx_g4_packed_bytes(rows, cols, group, zeros):
+        raise ValueError(f"packed: {packed.nbytes} bytes, expected {rfx_g4_packed_bytes(rows, cols, group, zeros)}")
+    codes = np.empty((rows, cols), dtype=np.uint8)
+    scales = np.empty((rows, cols // max(group, 1)), dtype=np.uint16)
+    z = np.empty(scales.shape, dtype=np.uint8) if zeros else None
+    _check(_g4_unpack(_ptr(packed), rows, cols, group, _ptr(codes), _ptr(scales), _ptr(z)))
+    return codes, scales, z
+
+
+def _bytes_at_least(name: str, t, n: int):
+    import torch
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: must be on the current CUDA device, not {t.device}")
+    if t.numel() * t.element_size() < n:
+        raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, at least {n} expected")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def rfx_g4_pack_device(codes, scales, zeros, rows: int, cols: int, group: int, dst, stream=None):
+    """Pack device tensors (codes uint8 [rows][cols], scales float16 and zeros uint8 or
+    None [rows][cols/group]) into device dst (rfx_g4_packed_bytes bytes)."""
+    import torch
+    _dense("codes", codes, (rows, cols), torch.uint8)
+    _dense("scales", scales, (rows, cols // max(group, 1)), torch.float16)
+    if zeros is not None:
+        _dense("zeros", zeros, (rows, cols // max(group, 1)), torch.uint8)
+    _bytes_at_least("dst", dst, rfx_g4_packed_bytes(rows, cols, group, zeros is not None))
+    _check(_g4_pack_device(_ptr(codes), _ptr(scales), _ptr(zeros), rows, cols, group, _ptr(dst), _stream(stream)))
+
+
+def rfx_gemv_g4(W, N: int, K: int, group: int, x, y, zeros: bool = False, stream=None):
+    """y fp32 [q][N] = W x for packed G4 weights W [N][K] and x [q][K] (bf16, fp16 or
+    fp32, q <= 8; device tensors).  zeros: W was packed with zero points."""
+    import torch
+    q = x.shape[0]
+    _dense("x", x, (q, K))
+    _dense("y", y, (q, N), torch.float32)
+    _bytes_at_least("W", W, rfx_g4_packed_bytes(N, K, group, zeros))
+    _check(_gemv_g4(_ptr(W), N, K, group, 1 if zeros else 0, _ptr(x), _rows_dtype(x), q, _ptr(y), _stream(stream)))
+
+
+def _experts_g4(x, offsets, y, N, K):
+    import torch
+    R, E = x.shape[0], offsets.shape[0] - 1
+    _dense("x", x, (R, K))
+    _dense("offsets", offsets, (E + 1,), torch.int32)
+    _dense("y", y, (R, N), torch.float32)
+    return R, E
+
+
+def moe_gemv_g4(W, stride: int, N: int, K: int, group: int, x, offsets, y, zeros: bool = False, stream=None):
+    """y[r] = W_e x[r] for the rows r of expert e (offsets int32 [E+1]): x [R][K] bf16,
+    fp16 or fp32, y fp32 [R][N], W: E packed G4 matrices `stride` bytes apart."""
+    R, E = _experts_g4(x, offsets, y, N, K)
+    _bytes_at_least("W", W, (E - 1) * stride + rfx_g4_packed_bytes(N, K, group, zeros))
+    _check(_moe_g4(_ptr(W), stride, E, N, K, group, 1 if zeros else 0, _ptr(x), _rows_dtype(x), _ptr(offsets), R,
+                   _ptr(y), _stream(stream)))
+
+
+def moe_gate_up_g4(gate, up, stride: int, N: int, K: int, group: int, x, offsets, h, zeros: bool = False, stream=None):
+    """h[r] = silu(gate_e x[r]) * (up_e x[r]) for the rows r of expert e; arguments as moe_gemv_g4."""
+    R, E = _experts_g4(x, offsets, h, N, K)
+    n = (E - 1) * stride + rfx_g4_packed_bytes(N, K, group, zeros)
+    _bytes_at_least("gate", gate, n)
+    _bytes_at_least("up", up, n)
+    _check(_moe_gate_up_g4(_ptr(gate), _ptr(up), stride, E, N, K, group, 1 if zeros else 0, _ptr(x), _rows_dtype(x),
+                           _ptr(offsets), R, _ptr(h), _stream(stream)))
 
 
 def moe_layer_create(desc: moe_layer_desc) -> int:

@@ -268,6 +268,85 @@ int moe_combine_rows_backward(const void* dy, rfx_dtype y_dtype, const void* ys,
 int rfx_gemv_q(rfx_format f, const void* W, int64_t N, int64_t K, const void* x, int x_is_fp32, int q,
                float* y, void* stream);
 
+/* ------------------------------------- 4-bit weights, group scales ------ */
+
+/*
+ * "G4" weights, the form most 4-bit checkpoints come in, beside the library's
+ * own block formats:
+ *   W[n][c] = scale[n][c / G] * (code[n][c] - zero[n][c / G])
+ * code: 4 bits; scale: binary16 per row and group of G = 32, 64 or 128 columns;
+ * zero: an integer 0..15 per row and group, or 8 everywhere where a matrix is packed
+ * without zeros (has_zeros = 0).  Per weight 4.5 / 4.25 / 4.125 bits, and 0.25 /
+ * 0.125 / 0.0625 more with zeros.
+ *
+ * Packed layout: rows padded to row-groups of 16 with zero codes and scales,
+ * each row-group a contiguous stream of chunks of 256 columns (the last one
+ * cols % 256).  A chunk of nc columns holds
+ *   codes:  ceil(nc / 64) slabs of 512 bytes, two 32-column tiles each; lane
+ *           L = 4g + t (g = 0..7, t = 0..3) owns bytes 16L .. 16L + 15 of a slab,
+ *           four little-endian words: (tile 0, row g), (tile 0, row g + 8),
+ *           (tile 1, row g), (tile 1, row g + 8).  Nibble i = 0..3 of a word
+ *           (bits 4i .. 4i + 3) is the code of column 8t + 2i of the tile, nibble
+ *           4 + i the code of column 8t + 2i + 1.  A missing tile 1 is zero.
+ *   scales: [nc / G][8] words, word g = scale of row g | scale of row g + 8 << 16
+ *   zeros:  (has_zeros) [nc / G][8] bytes, byte g = zero of row g | zero of row
+ *           g + 8 << 4, padded with zero bytes to a multiple of 16
+ */
+
+/* Bytes of a packed matrix; 0 for a bad group, rows outside [0, 2^31), or cols
+ * that is not a positive multiple of group (at most 2^30). */
+size_t rfx_g4_packed_bytes(int64_t rows, int64_t cols, int group, int has_zeros);
+
+/*
+ * Host packer.  codes: host uint8 [rows][cols], each < 16; scales: host binary16
+ * bits [rows][cols / group], finite; zeros: host uint8 [rows][cols / group], each < 16,
+ * or NULL (has_zeros = 0).  Returns RFX_EINVAL on any bad value (dst is then unchanged).
+ */
+int rfx_g4_pack(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t rows, int64_t cols,
+                int group, void* dst, size_t dst_bytes);
+
+/* Host inverse of rfx_g4_pack; zeros NULL for a matrix packed without them. */
+int rfx_g4_unpack(const void* src, int64_t rows, int64_t cols, int group, uint8_t* codes, uint16_t* scales,
+                  uint8_t* zeros);
+
+/*
+ * Device packer: the same layout, all pointers in device memory (dst 16-byte
+ * aligned), asynchronous on stream.  Values are not checked: codes and zeros are
+ * taken modulo 16.  Matrices of rows % 16 == 0 may be packed as one of all their rows.
+ */
+int rfx_g4_pack_device(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t rows, int64_t cols,
+                       int group, void* dst, void* stream);
+
+/*
+ * y[c][n] = sum_k W[n][k] x[c][k] for c < q: rfx_gemv_q for G4 weights.  W:
+ * device, packed [N][K], 16-byte aligned.  x: device [q][K] of x_dtype, 16-byte
+ * aligned.  y: device fp32 [q][N].  The products (code - zero) * x are exact for
+ * every x_dtype and are summed in fp32 within a group; each group's sum is scaled and
+ * added in fp32.  A non-finite x makes its column non-finite and no other.
+ * Limits: 1 <= q <= 8, N >= 1, K % group == 0.  One launch, no workspace.
+ */
+int rfx_gemv_g4(const void* W, int64_t N, int64_t K, int group, int has_zeros, const void* x, rfx_dtype x_dtype, int q,
+                float* y, void* stream);
+
+/*
+ * The experts' products over rows grouped by expert (moe_group_tokens' xs and
+ * offsets): for the rows r of expert e, offsets[e] <= r < offsets[e + 1],
+ *   moe_gemv_g4:     y[r] = W_e x[r]
+ *   moe_gate_up_g4:  h[r] = silu(gate_e x[r]) * (up_e x[r]), silu(z) = z / (1 + e^-z)
+ * W_e is at W + e * stride (bytes, a multiple of 16), packed [N][K].  x: device
+ * [R][K] of x_dtype, 16-byte aligned; offsets: device int32 [E + 1], ascending, read on the
+ * device (values outside [0, R] are taken as the nearer end); y, h: device fp32
+ * [R][N], rows outside every expert left as they were.  R: rows of x (T * k).
+ * A pass over an expert's weights serves up to 8 of its rows; only experts with
+ * rows are read.  Meant for decode and verify (few rows an expert).  Numerics as rfx_gemv_g4.  Limits:
+ * 1 <= E <= 1024, R >= 0 (R = 0 is a no-op), N >= 1, K % group == 0.  One launch, no workspace.
+ */
+int moe_gemv_g4(const void* W, size_t stride, int E, int64_t N, int64_t K, int group, int has_zeros, const void* x,
+                rfx_dtype x_dtype, const int32_t* offsets, int R, float* y, void* stream);
+int moe_gate_up_g4(const void* gate, const void* up, size_t stride, int E, int64_t N, int64_t K, int group,
+                   int has_zeros, const void* x, rfx_dtype x_dtype, const int32_t* offsets, int R, float* h,
+                   void* stream);
+
 /* ------------------------------------------------------------ MoE FFN --- */
 
 /*

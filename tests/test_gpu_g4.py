@@ -1,0 +1,346 @@
+"""4-bit group-scale products against 64-bit sums.
+
+Two kinds of check.  Integer inputs (x small integers, scales powers of two):
+every sum is an integer multiple of the scale below 2^24 in size, so fp32 holds
+every partial sum and the result must be equal bit for bit, in any order.
+Random inputs: an m16n8k16 step adds 16 products to its accumulator; if the
+tensor core cut each addend to 24 bits of the largest one, a step would err by
+at most 16 * 2^-23 times the magnitude M = sum |w x|.  K / 16 steps (three
+times that for fp32 x, whose parts add up to at most 1.01 |x|) then stay below
+3 * K * 2^-23 * M, and scaling and adding the groups and the warps' shares adds
+(K / G + 17) * 2^-24 * M; beside that bound the library's acceptance holds,
+relative L2 <= 1e-5.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_moe_rocmfpx_b200 as rfx
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, HF, FF = torch.bfloat16, torch.float16, torch.float32
+
+
+class G4:
+    """E random matrices [N][K], packed `stride` bytes apart, and their 64-bit values."""
+
+    def __init__(self, N, K, G, zeros, seed, E=1, integer=False, pad=0):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(seed)
+        self.N, self.K, self.G, self.zeros, self.E = N, K, G, zeros, E
+        self.stride = rfx.rfx_g4_packed_bytes(N, K, G, zeros) + pad
+        self.codes = torch.randint(0, 16, (E, N, K), generator=g, device=DEV, dtype=torch.uint8)
+        u = torch.rand((E, N, K // G), generator=g, device=DEV)
+        self.scales = (torch.exp2(torch.floor(u * 3) - 1) if integer else 0.01 * torch.exp2(2 * u - 1)).half()
+        self.z = torch.randint(0, 16, self.scales.shape, generator=g, device=DEV, dtype=torch.uint8) if zeros else None
+        self.packed = torch.full((E * self.stride,), 0xA5, dtype=torch.uint8, device=DEV)
+        for e in range(E):
+            rfx.rfx_g4_pack_device(self.codes[e], self.scales[e], self.z[e] if zeros else None, N, K, G,
+                                   self.packed[e * self.stride:])
+
+    def dense(self, e=0):
+        c = self.codes[e].double().view(self.N, -1, self.G)
+        z = self.z[e].double()[..., None] if self.zeros else 8.0
+        return ((c - z) * self.scales[e].double()[..., None]).view(self.N, self.K)
+
+
+def x_of(shape, dtype, seed, integer):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    if integer:
+        return torch.randint(-8, 9, shape, generator=g, device=DEV).to(dtype)
+    return torch.randn(shape, generator=g, device=DEV).to(dtype)
+
+
+def check(y, W, x, G, integer=False):
+    ref = x.double() @ W.t()
+    if integer:
+        assert torch.equal(y.double(), ref)
+        return
+    K = x.shape[1]
+    m = x.double().abs() @ W.abs().t()
+    err = (y.double() - ref).abs()
+    assert torch.isfinite(y).all()
+    assert bool((err <= (3 * K * 2.0 ** -23 + (K / G + 17) * 2.0 ** -24) * m + 1e-37).all())
+    assert float((y.double() - ref).norm() / ref.norm()) <= 1e-5
+
+
+SHAPES = [(1, 32, 32), (16, 64, 64), (17, 288, 32), (33, 128, 128), (100, 320, 64), (64, 4096, 128), (250, 2048, 32),
+          (4096, 256, 64), (5000, 96, 32), (48, 14336, 128), (31, 7168, 64), (20000, 512, 128)]
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("N,K,G", SHAPES)
+def test_device_pack_equals_host_pack(N, K, G, zeros):
+    w = G4(N, K, G, zeros, N)
+    host = rfx.rfx_g4_pack(w.codes[0].cpu().numpy(), w.scales[0].cpu().numpy(), G,
+                           w.z[0].cpu().numpy() if zeros else None)
+    assert np.array_equal(w.packed.cpu().numpy(), host)
+    # codes at an odd address, and values above 15 taken modulo 16
+    raw = torch.zeros(N * K + 3, dtype=torch.uint8, device=DEV)
+    raw[3:] = w.codes[0].flatten() | 0xC0
+    again = torch.zeros_like(w.packed)
+    rfx.rfx_g4_pack_device(raw[3:].view(N, K), w.scales[0], w.z[0] if zeros else None, N, K, G, again)
+    assert torch.equal(again, w.packed)
+
+
+@pytest.mark.parametrize("integer", [True, False])
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("N,K,G", SHAPES)
+def test_gemv(N, K, G, zeros, dtype, integer):
+    w = G4(N, K, G, zeros, N + K, integer=integer)
+    W = w.dense()
+    for q in (1, 3, 8):
+        x = x_of((q, K), dtype, q, integer)
+        out = torch.full((q * N + 64,), float("nan"), device=DEV)
+        y = out[:q * N].view(q, N)
+        rfx.rfx_gemv_g4(w.packed, N, K, G, x, y, zeros=zeros)
+        check(y, W, x, G, integer)
+        assert torch.isnan(out[q * N:]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+def test_gemv_columns_are_independent(dtype):
+    N, K, G = 300, 1024, 64
+    w = G4(N, K, G, True, 5)
+    x = x_of((8, K), dtype, 1, False)
+    y8 = torch.empty((8, N), device=DEV)
+    rfx.rfx_gemv_g4(w.packed, N, K, G, x, y8, zeros=True)
+    for c in (0, 3, 7):
+        y1 = torch.empty((1, N), device=DEV)
+        rfx.rfx_gemv_g4(w.packed, N, K, G, x[c:c + 1].contiguous(), y1, zeros=True)
+        assert torch.equal(y1[0], y8[c])
+    bad = x.clone()
+    bad[2, 17], bad[5, 1000] = float("nan"), float("inf")
+    yb = torch.empty((8, N), device=DEV)
+    rfx.rfx_gemv_g4(w.packed, N, K, G, bad, yb, zeros=True)
+    keep = [0, 1, 3, 4, 6, 7]
+    assert torch.equal(yb[keep], y8[keep])
+    assert torch.isnan(yb[2]).all() and not torch.isfinite(yb[5]).any()
+
+
+def test_gemv_fp32_x_of_any_size():
+    # 24-bit significands from 2^-60 to 2^60 in one row: the parts lose nothing
+    N, K, G = 64, 512, 32
+    w = G4(N, K, G, True, 8)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    for lo, hi in ((-60, -40), (0, 1), (40, 60)):
+        x = torch.randn((4, K), generator=g, device=DEV) * torch.exp2(
+            torch.randint(lo, hi, (4, K), generator=g, device=DEV).float())
+        y = torch.empty((4, N), device=DEV)
+        rfx.rfx_gemv_g4(w.packed, N, K, G, x, y, zeros=True)
+        check(y, w.dense(), x, G)
+    # one column of x at a time picks one weight: x * w exactly rounded
+    x = torch.zeros((8, K), device=DEV)
+    v = torch.tensor([1 + 2.0 ** -23, 3.1415927, -0.1, 1e-30, 7e25, 16777215.0, -1.9999999, 2.0 ** -100], device=DEV)
+    cols = [0, 31, 32, 77, 255, 256, 300, 511]
+    for i, c in enumerate(cols):
+        x[i, c] = v[i]
+    y = torch.empty((8, N), device=DEV)
+    rfx.rfx_gemv_g4(w.packed, N, K, G, x, y, zeros=True)
+    W = w.dense()
+    want = torch.stack([W[:, c] * v[i].double() for i, c in enumerate(cols)])
+    # (code - zero) * x needs up to 28 bits: one rounding to fp32, one more for the scale
+    assert bool(((y.double() - want).abs() <= 4 * 2.0 ** -23 * want.abs()).all())
+
+
+# ------------------------------------------------------------- experts ---
+
+def offsets_of(counts):
+    off = torch.zeros(len(counts) + 1, dtype=torch.int32)
+    off[1:] = torch.cumsum(torch.tensor(counts), 0)
+    return off.to(DEV)
+
+
+COUNTS = {"one": [1], "first_last": [1, 0, 0, 2], "wide": [0, 9, 0, 0, 23, 8, 1, 0], "empty": [0, 0, 0],
+          "all": [3, 1, 2, 1, 4, 1]}
+
+
+@pytest.mark.parametrize("integer", [True, False])
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("N,K,G,zeros", [(64, 256, 128, False), (50, 352, 32, True), (300, 2048, 64, True)])
+@pytest.mark.parametrize("which", sorted(COUNTS))
+def test_expert_products(which, N, K, G, zeros, dtype, integer):
+    counts = COUNTS[which]
+    E, R = len(counts), sum(counts) + 3        # three rows behind the last expert
+    w = G4(N, K, G, zeros, 3, E=E, integer=integer, pad=48)
+    off = offsets_of(counts)
+    x = x_of((R, K), dtype, 4, integer)
+    x[R - 3:] = float("nan")
+    y = torch.full((R, N), -5.0, device=DEV)
+    rfx.moe_gemv_g4(w.packed, w.stride, N, K, G, x, off, y, zeros=zeros)
+    lo = 0
+    for e, n in enumerate(counts):
+        if n:
+            check(y[lo:lo + n], w.dense(e), x[lo:lo + n], G, integer)
+        lo += n
+    assert (y[lo:] == -5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("N,K,G,zeros", [(64, 256, 128, True), (50, 352, 32, False), (300, 2048, 64, True)])
+@pytest.mark.parametrize("which", sorted(COUNTS))
+def test_gate_up(which, N, K, G, zeros, dtype):
+    counts = COUNTS[which]
+    E, R = len(counts), sum(counts) + 1
+    gate, up = G4(N, K, G, zeros, 11, E=E), G4(N, K, G, zeros, 12, E=E)
+    off = offsets_of(counts)
+    x = x_of((R, K), dtype, 6, False)
+    h = torch.full((R, N), -5.0, device=DEV)
+    rfx.moe_gate_up_g4(gate.packed, up.packed, gate.stride, N, K, G, x, off, h, zeros=zeros)
+    d = 3 * K * 2.0 ** -23 + (K / G + 17) * 2.0 ** -24
+    lo = 0
+    for e, n in enumerate(counts):
+        if n:
+            xe = x[lo:lo + n].double()
+            g, u = xe @ gate.dense(e).t(), xe @ up.dense(e).t()
+            mg, mu = xe.abs() @ gate.dense(e).abs().t(), xe.abs() @ up.dense(e).abs().t()
+            want = g * torch.sigmoid(g) * u
+            # |silu'| < 1.1 and |silu(g)| <= |g|: the products' errors, then four roundings and expf's 2 ulp
+            bound = 1.1 * d * mg * u.abs() + d * mu * g.abs() + 1.1 * d * d * mg * mu + 8 * 2.0 ** -23 * want.abs()
+            got = h[lo:lo + n].double()
+            assert bool(((got - want).abs() <= bound + 1e-37).all())
+            assert float((got - want).norm() / want.norm()) <= 1e-5
+        lo += n
+    assert (h[lo:] == -5.0).all()
+
+
+def test_gate_up_far_tail_of_silu():
+    # one weight per row picks g and u: silu at the ends of fp32's range of exp
+    N, K, G = 16, 32, 32
+    codes = torch.full((N, K), 8, dtype=torch.uint8, device=DEV)
+    codes[:, 0] = 9                                  # weight 1 in column 0
+    s = torch.ones((N, 1), dtype=torch.float16, device=DEV)
+    packed = torch.zeros(rfx.rfx_g4_packed_bytes(N, K, G), dtype=torch.uint8, device=DEV)
+    rfx.rfx_g4_pack_device(codes, s, None, N, K, G, packed)
+    x = torch.zeros((6, K), device=DEV)
+    x[:, 0] = torch.tensor([0.0, -87.0, -95.0, 88.0, 3000.0, -3000.0])
+    h = torch.empty((6, N), device=DEV)
+    rfx.moe_gate_up_g4(packed, packed, packed.numel(), N, K, G, x, offsets_of([6]), h)
+    v = x[:, :1].double()
+    want = (v * v / (1 + torch.exp(-v))).expand(6, N)
+    # exp(g) near -90 carries |g| * 2^-24 * 2 of its argument's rounding
+    assert bool(((h.double() - want).abs() <= 4e-5 * want.abs() + 1e-38).all())
+
+
+def test_expert_products_many_experts_and_bad_offsets():
+    E, N, K, G = 1024, 32, 64, 32
+    w = G4(N, K, G, False, 2, E=1, integer=True)
+    packed = w.packed.repeat(E)
+    counts = [0] * E
+    for e in (0, 1, 511, 777, 1023):
+        counts[e] = 1 + e % 3
+    R = sum(counts)
+    x = x_of((R, K), BF, 1, True)
+    y = torch.empty((R, N), device=DEV)
+    rfx.moe_gemv_g4(packed, w.stride, N, K, G, x, offsets_of(counts), y)
+    check(y, w.dense(), x, G, integer=True)
+    # offsets outside [0, R] are taken as the nearer end, a descending pair as no rows
+    off = torch.tensor([-4, 2, 1, R + 9], dtype=torch.int32, device=DEV)
+    y2 = torch.full((R, N), -5.0, device=DEV)
+    rfx.moe_gemv_g4(packed, w.stride, N, K, G, x, off, y2)
+    assert torch.equal(y2, y)
+
+
+def test_python_checks_on_the_device():
+    w = G4(32, 64, 32, False, 1)
+    x, y = x_of((2, 64), BF, 1, False), torch.empty((2, 32), device=DEV)
+    for bad in ({"x": x[:, :32]}, {"x": x.t().contiguous().t()}, {"y": y.half()}, {"x": x.double()}, {"y": y.cpu()},
+                {"W": w.packed[:-1]}):
+        a = {"W": w.packed, "x": x, "y": y, **bad}
+        with pytest.raises(ValueError):
+            rfx.rfx_gemv_g4(a["W"], 32, 64, 32, a["x"], a["y"])
+    with pytest.raises(ValueError):                   # packed without zeros, read with
+        rfx.rfx_gemv_g4(w.packed, 32, 64, 32, x, y, zeros=True)
+
+
+# ------------------------------------------------- the operators together ---
+
+def moe_step(x, logits, gate, up, down, k, base, bufs):
+    """Route, group, gate/up, down and combine with 4-bit experts."""
+    H, I, E = down.N, gate.N, gate.E
+    rfx.moe_router_topk(logits, k, bufs["idx"], bufs["w"])
+    rfx.moe_group_tokens(x, bufs["idx"], E, bufs["xs"], bufs["pos"], bufs["rows"], bufs["off"], bufs["ws"])
+    rfx.moe_gate_up_g4(gate.packed, up.packed, gate.stride, I, H, gate.G, bufs["xs"], bufs["off"], bufs["h"],
+                       zeros=gate.zeros)
+    rfx.moe_gemv_g4(down.packed, down.stride, H, I, down.G, bufs["h"], bufs["off"], bufs["d"], zeros=down.zeros)
+    rfx.moe_combine_rows(bufs["d"], bufs["pos"], bufs["w"], bufs["y"], base=base)
+
+
+def make_bufs(T, k, E, H, I):
+    i32 = dict(dtype=torch.int32, device=DEV)
+    R = T * k
+    return {"idx": torch.empty((T, k), **i32), "w": torch.empty((T, k), device=DEV),
+            "xs": torch.empty((R, H), dtype=BF, device=DEV), "pos": torch.empty((T, k), **i32),
+            "rows": torch.empty(R, **i32), "off": torch.empty(E + 1, **i32), "h": torch.empty((R, I), device=DEV),
+            "d": torch.empty((R, H), device=DEV), "y": torch.empty((T, H), device=DEV),
+            "ws": torch.zeros(rfx.moe_group_workspace_bytes(T, k, E), dtype=torch.uint8, device=DEV)}
+
+
+@pytest.mark.parametrize("T", [1, 4, 40])
+def test_moe_step_and_its_router_gradient(T):
+    H, I, E, k = 512, 256, 8, 2
+    gate, up, down = (G4(n, c, 64, True, s, E=E) for n, c, s in ((I, H, 1), (I, H, 2), (H, I, 3)))
+    x = x_of((T, H), BF, T, False)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    logits = torch.randn((T, E), generator=g, device=DEV)
+    base = torch.randn((T, H), generator=g, device=DEV)
+    b = make_bufs(T, k, E, H, I)
+    moe_step(x, logits, gate, up, down, k, base, b)
+    assert rfx.rfx_ws_status(b["ws"]) == rfx.RFX_OK
+    dy = torch.randn((T, H), generator=g, device=DEV)
+    dd, dw, dl = torch.empty_like(b["d"]), torch.empty_like(b["w"]), torch.empty_like(logits)
+    rfx.moe_combine_rows_backward(dy, b["d"], b["pos"], b["w"], dd, dw)
+    rfx.moe_router_topk_backward(b["idx"], b["w"], dw, dl)
+    # the same in 64 bits through autograd, experts frozen
+    l64 = logits.double().requires_grad_()
+    sel = torch.topk(l64, k, dim=1)
+    assert torch.equal(sel.indices.int(), b["idx"])
+    w = torch.softmax(sel.values, dim=1)
+    y = base.double()
+    for t in range(T):
+        for j in range(k):
+            e = int(sel.indices[t, j])
+            gg, uu = gate.dense(e) @ x[t].double(), up.dense(e) @ x[t].double()
+            hh = gg * torch.sigmoid(gg) * uu
+            y = y.index_add(0, torch.tensor([t], device=DEV), (w[t, j] * (down.dense(e) @ hh))[None])
+    assert float((b["y"].double() - y.detach()).norm() / y.detach().norm()) <= 1e-5
+    y.backward(dy.double())
+    assert float((dl.double() - l64.grad).norm() / l64.grad.norm()) <= 1e-4
+
+
+def test_moe_step_in_a_graph_and_two_streams_at_once():
+    H, I, E, k, T = 1024, 256, 16, 4, 8
+    gate, up, down = (G4(n, c, 32, False, s, E=E) for n, c, s in ((I, H, 1), (I, H, 2), (H, I, 3)))
+    xa, xb = x_of((T, H), BF, 1, False), x_of((T, H), BF, 2, False)
+    la, lb = (torch.randn((T, E), device=DEV) for _ in range(2))
+    a, b = make_bufs(T, k, E, H, I), make_bufs(T, k, E, H, I)
+    moe_step(xa, la, gate, up, down, k, None, a)
+    moe_step(xb, lb, gate, up, down, k, None, b)
+    torch.cuda.synchronize()
+    ya, yb = a["y"].clone(), b["y"].clone()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        a["y"].zero_()
+        b["y"].zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s1):
+            moe_step(xa, la, gate, up, down, k, None, a)
+        with torch.cuda.stream(s2):
+            moe_step(xb, lb, gate, up, down, k, None, b)
+        torch.cuda.synchronize()
+        assert torch.equal(a["y"], ya) and torch.equal(b["y"], yb)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe_step(xa, la, gate, up, down, k, None, a)
+    xa.copy_(xb)
+    la.copy_(lb)
+    for _ in range(3):
+        a["y"].zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a["y"], yb)
