@@ -1,18 +1,27 @@
-// g4.cuh -- products with 4-bit weights in groups (layout: g4_layout.h), for
-// up to 8 columns a pass: y[c][n] = sum_g scale[n][g] sum_k (code - zero) x[c][k].
+// g4.cuh -- products with 4-bit weights in groups (layout: g4_layout.h):
+//   y[c][n] = sum_g scale[n][g] sum_k (code - zero) x[c][k].
 //
-// The bracket is taken on the tensor cores (mma.sync m16n8k16, 16 rows x 8
-// columns) with exact operands: code - zero is a small integer, formed in
-// registers by or-ing the code into the mantissa of 128 (bf16) or 1024 (fp16)
-// and subtracting 128 + zero or 1024 + zero; x enters as it is (bf16, fp16) or
-// as three bf16 parts that add up to it (fp32).  So the only roundings are the
-// fp32 sums and the scale's product.
+// The inner sums run on the tensor cores as fp16 products (mma.sync m16n8k16,
+// 16 rows x 8 columns, fp32 sums) with exact operands.
+//   Codes: a 16-bit half whose bits 3..6 (or 7..10) are a code and whose other bits are
+//   zero is, as fp16, 8 (or 128) code * 2^-24: subnormal or, for both values of bit
+//   10, of the lowest exponent, which has the same scale.  The four codes of a half
+//   lie so that the half and the half turned by a byte have one at either place: a PRMT and
+//   four ANDs make eight operands of a word, and the x that meet codes at bits 7..10 are
+//   stored divided by 16.
+//   x: brought to max|x| in [2^13, 2^14) by a power of two (per column and warp's part
+//   of K) and rounded to fp16.  That keeps bf16 and fp16 values whole down to
+//   2^-23 of the largest, and 2^-35 of the largest below that.  fp32 x is cut into
+//   three such parts of 11 bits, which are columns of the product.
+//   zero: the sums start from -zero * sum_k x.
+// So the only roundings that count are the fp32 sums and the scale's product.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "g4.h"
 #include "g4_layout.h"
@@ -22,259 +31,592 @@
 namespace rfx {
 namespace {
 
-constexpr int G4_THREADS = 512;
-constexpr int G4_WARPS = G4_THREADS / 32;
+constexpr int G4_NR = 2;                        // row-groups a warp takes at a time
 constexpr int G4_MAXE = 1024;
+constexpr int G4_STAGES = 2;                    // chunk pairs of a warp's ring
+constexpr int G4_SMEM = 232448 - 1024;          // dynamic and static shared memory of a block, less what the system takes
 
-__device__ __forceinline__ uint32_t g4_bf16_sub(uint32_t a, uint32_t b) {
-    __nv_bfloat162 x, y;
-    memcpy(&x, &a, 4);
-    memcpy(&y, &b, 4);
-    x = __hsub2(x, y);
-    memcpy(&a, &x, 4);
-    return a;
-}
-__device__ __forceinline__ uint32_t g4_f16_sub(uint32_t a, uint32_t b) {
-    __half2 x, y;
-    memcpy(&x, &a, 4);
-    memcpy(&y, &b, 4);
-    x = __hsub2(x, y);
-    memcpy(&a, &x, 4);
-    return a;
-}
-// a / 16 - b, exact here
-__device__ __forceinline__ uint32_t g4_f16_sub16(uint32_t a, uint32_t b) {
-    __half2 x, y;
-    memcpy(&x, &a, 4);
-    memcpy(&y, &b, 4);
-    x = __hfma2(x, __float2half2_rn(0.0625f), __hneg2(y));
-    memcpy(&a, &x, 4);
-    return a;
-}
-
-// The four A registers of one word: codes 2i, 2i + 1 of the lane minus z, as
-// bf16 or fp16 pairs.
-template <bool F16>
-__device__ __forceinline__ void g4_unpack(uint32_t w, uint32_t z, uint32_t a[4]) {
-    if constexpr (F16) {
-        const uint32_t lo = 0x64006400u + z * 0x00010001u;            // 1024 + z
-        const uint32_t hi = 0x54005400u + z * 0x00100010u;            // 64 + z
-        const uint32_t w8 = w >> 8;
-        a[0] = g4_f16_sub((w & 0x000F000Fu) | 0x64006400u, lo);
-        a[1] = g4_f16_sub16((w & 0x00F000F0u) | 0x64006400u, hi);
-        a[2] = g4_f16_sub((w8 & 0x000F000Fu) | 0x64006400u, lo);
-        a[3] = g4_f16_sub16((w8 & 0x00F000F0u) | 0x64006400u, hi);
-    } else {
-        const uint32_t c = 0x43004300u + z * 0x00010001u;             // 128 + z
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = g4_bf16_sub(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, c);
-    }
-}
-
-// The B operands of one tile for the lane: columns 8t .. 8t + 7 of its x row.
-// fp32 x = p0 + p1 + p2 with bf16 parts cut off the top of the significand
-// (8 + 8 + 8 bits), so the three products add up to the exact one.
-template <int XT>
-struct G4B {
+// x in shared memory, for the columns (rows of x) of one or more passes.  A row of
+// it is a column, or (fp32) one of a column's three parts; a product (8 columns) takes the
+// columns of one pass, at most 8, or 2 of them with their parts (parts 0, 1, 2 and
+// a column that does not count).  A chunk: [tile][row][t][8 values], then -sum of each
+// group [group][product][8 columns], fp32 (times 2^-21, and times 8 without zeros).
+template <int XT> struct G4X {
     static constexpr int PARTS = XT == 1 ? 3 : 1;
-    uint32_t v[PARTS][4];
-    __device__ __forceinline__ void load(const void* x, long long at, bool live) {
-        if constexpr (XT != 1) {
-            uint4 q = {0u, 0u, 0u, 0u};
-            if (live) q = __ldg(reinterpret_cast<const uint4*>((const uint16_t*)x + at));
-            v[0][0] = q.x; v[0][1] = q.y; v[0][2] = q.z; v[0][3] = q.w;
+    static constexpr int COLS = XT == 1 ? 2 : 8;
+    static constexpr int BYTES = XT == 1 ? 4 : 2;
+    static constexpr int WARPS = XT == 1 ? 16 : 24;
+};
+__host__ __device__ constexpr int g4_x_bytes(int G, int products, int rows) {
+    return rows * (G4_CHUNK * 2) + G4_CHUNK / G * products * 32;
+}
+
+__device__ __forceinline__ void g4_cp16(uint32_t dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// (w & mask) | base in one instruction
+__device__ __forceinline__ uint32_t g4_field(uint32_t w, uint32_t mask, uint32_t base) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(base));
+    return d;
+}
+
+__device__ __forceinline__ void g4_mma(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1, const float c[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+// Four x values from k on, as fp32.
+template <int XT>
+__device__ __forceinline__ void g4_load_x(const uint8_t* x, float v[4]) {
+    if constexpr (XT == 1) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(x));
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(x));
+        if constexpr (XT == 0) {
+            v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xFFFF0000u);
+            v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xFFFF0000u);
         } else {
-            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (live) {
-                const float4 a = __ldg(reinterpret_cast<const float4*>((const float*)x + at));
-                const float4 b = __ldg(reinterpret_cast<const float4*>((const float*)x + at) + 1);
-                f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-                f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t u0 = __float_as_uint(f[2 * i]), u1 = __float_as_uint(f[2 * i + 1]);
-                v[0][i] = __byte_perm(u0, u1, 0x7632);
-                float r0 = f[2 * i] - __uint_as_float(u0 & 0xFFFF0000u);
-                float r1 = f[2 * i + 1] - __uint_as_float(u1 & 0xFFFF0000u);
-                u0 = __float_as_uint(r0);
-                u1 = __float_as_uint(r1);
-                v[1][i] = __byte_perm(u0, u1, 0x7632);
-                r0 -= __uint_as_float(u0 & 0xFFFF0000u);
-                r1 -= __uint_as_float(u1 & 0xFFFF0000u);
-                v[2][i] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
-            }
+            __half2 a, b;
+            memcpy(&a, &q.x, 4);
+            memcpy(&b, &q.y, 4);
+            const float2 f = __half22float2(a), h = __half22float2(b);
+            v[0] = f.x; v[1] = f.y; v[2] = h.x; v[3] = h.y;
         }
     }
-};
+}
 
-// One chunk of nc columns of two row-groups into acc.
-template <int XT, int G, bool Z>
-__device__ __forceinline__ void g4_chunk(const uint8_t* c0, const uint8_t* c1, int nc, const void* x, long long xat,
-                                         bool live, int lane, float acc[2][4]) {
-    constexpr bool F16 = XT == 2;
-    const int g = lane >> 2;
-    const int soff = g4_scale_off(nc), zoff = g4_zero_off(nc, G);
-    const uint8_t* const ch[2] = {c0, c1};
-    float s[2][4];
+// The lane's part of a chunk of G4_NR row-groups, from its stage.
+template <int G, bool Z>
+struct G4Stage {
+    static constexpr int NG = G4_CHUNK / G, FULL = g4_chunk_bytes(G4_CHUNK, G, Z);
+    uint4 w[G4_NR][2];
+    uint32_t s[G4_NR][NG];   // scales of rows g and g + 8
+    uint32_t z[G4_NR];       // a byte per group: zeros of rows g and g + 8
+
+    __device__ __forceinline__ void load(const uint8_t* st, int nc, int lane) {
+        const int g = lane >> 2;
+        if (nc >= G4_CHUNK) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        if (p * 64 < nc) {
-            uint4 w[2];
+            for (int i = 0; i < G4_NR; ++i) {
+                const uint8_t* r = st + i * FULL;
+                w[i][0] = *reinterpret_cast<const uint4*>(r + lane * 16);
+                w[i][1] = *reinterpret_cast<const uint4*>(r + 512 + lane * 16);
+                const uint8_t* sc = r + g4_scale_off(G4_CHUNK) + g * (4 * NG);
+                if constexpr (NG == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(sc);
+                    s[i][0] = v.x; s[i][1] = v.y; s[i][2] = v.z; s[i][3] = v.w;
+                } else if constexpr (NG == 2) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(sc);
+                    s[i][0] = v.x; s[i][1] = v.y;
+                } else {
+                    s[i][0] = *reinterpret_cast<const uint32_t*>(sc);
+                }
+                if constexpr (Z) {
+                    const uint8_t* zp = r + g4_zero_off(G4_CHUNK, G) + g * NG;
+                    if constexpr (NG == 4) z[i] = *reinterpret_cast<const uint32_t*>(zp);
+                    else if constexpr (NG == 2) z[i] = *reinterpret_cast<const uint16_t*>(zp);
+                    else z[i] = *zp;
+                }
+            }
+        } else {   // the last chunk of a K that is no multiple of 128: what is missing counts as zero
+            const int ng = nc / G;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) w[r] = *reinterpret_cast<const uint4*>(ch[r] + p * 512 + lane * 16);
+            for (int i = 0; i < G4_NR; ++i) {
+                const uint8_t* r = st + i * FULL;
+                w[i][0] = *reinterpret_cast<const uint4*>(r + lane * 16);
+                w[i][1] = make_uint4(0u, 0u, 0u, 0u);
+                if (nc > 64) w[i][1] = *reinterpret_cast<const uint4*>(r + 512 + lane * 16);
+                z[i] = 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int col = p * 64 + h * 32;
-                if (col < nc) {
-                    G4B<XT> b;
-                    b.load(x, xat + col, live);
-                    const int grp = col / G;
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        if (col % G == 0)
-                            for (int i = 0; i < 4; ++i) s[r][i] = 0.f;
-                        uint32_t z0 = 8, z1 = 8;
-                        if constexpr (Z) {
-                            const uint32_t zz = ch[r][zoff + grp * 8 + g];
-                            z0 = zz & 15u;
-                            z1 = zz >> 4;
-                        }
-                        uint32_t a0[4], a1[4];
-                        g4_unpack<F16>(h ? w[r].z : w[r].x, z0, a0);
-                        g4_unpack<F16>(h ? w[r].w : w[r].y, z1, a1);
-                        const uint32_t m0[4] = {a0[0], a1[0], a0[1], a1[1]};
-                        const uint32_t m1[4] = {a0[2], a1[2], a0[3], a1[3]};
-#pragma unroll
-                        for (int q = 0; q < G4B<XT>::PARTS; ++q) {
-                            mma16816<F16>(s[r], m0, b.v[q][0], b.v[q][1], s[r]);
-                            mma16816<F16>(s[r], m1, b.v[q][2], b.v[q][3], s[r]);
-                        }
-                        if ((col + 32) % G == 0) {
-                            const __half2 sc = *reinterpret_cast<const __half2*>(ch[r] + soff + (grp * 8 + g) * 4);
-                            const float2 f = __half22float2(sc);
-                            acc[r][0] = fmaf(f.x, s[r][0], acc[r][0]);
-                            acc[r][1] = fmaf(f.x, s[r][1], acc[r][1]);
-                            acc[r][2] = fmaf(f.y, s[r][2], acc[r][2]);
-                            acc[r][3] = fmaf(f.y, s[r][3], acc[r][3]);
-                        }
+                for (int j = 0; j < NG; ++j) {
+                    s[i][j] = 0;
+                    if (j < ng) {
+                        s[i][j] = reinterpret_cast<const uint32_t*>(r + g4_scale_off(nc))[g * ng + j];
+                        if (Z) z[i] |= (uint32_t)r[g4_zero_off(nc, G) + g * ng + j] << (8 * j);
                     }
                 }
             }
         }
     }
+};
+
+// A chunk of G4_NR row-groups into acc; xs: the chunk's x, at[nb] the lane's place
+// in a tile of it, tile the bytes of a tile; sums: the lane's sums of the first group,
+// sum_step bytes to the next.
+template <int G, bool Z, int NB>
+__device__ __forceinline__ void g4_chunk(const G4Stage<G, Z>& st, const uint8_t* xs, const int at[NB], int tile,
+                                         const uint8_t* sums, int sum_step, float acc[G4_NR][NB][4]) {
+    constexpr int NG = G4_CHUNK / G;
+    float s[G4_NR][NB][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {      // tiles of 32 columns
+        const int j = k * 32 / G;      // the group
+        if (k * 32 % G == 0) {
+            float z[G4_NR][2];
+#pragma unroll
+            for (int r = 0; r < G4_NR; ++r) {
+                z[r][0] = z[r][1] = 1.f;
+                if constexpr (Z) {   // as floats: or-ed into the mantissa of 2^23, there worth z or 16 z times 256^(j % 2)
+                    const uint32_t zz = j >= 2 ? st.z[r] >> 16 : st.z[r], magic = 0x4B000000u;
+                    const float f = j & 1 ? 0x1.0p-8f : 1.f;
+                    z[r][0] = fmaf(__uint_as_float(g4_field(zz, j & 1 ? 0xF00u : 0xFu, magic)), f, -8388608.f * f);
+                    z[r][1] = fmaf(__uint_as_float(g4_field(zz, j & 1 ? 0xF000u : 0xF0u, magic)), f * 0.0625f,
+                                   -524288.f * f);
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float2 sx = *reinterpret_cast<const float2*>(sums + j * sum_step + b * 32);
+#pragma unroll
+                for (int r = 0; r < G4_NR; ++r) {
+                    s[r][b][0] = Z ? z[r][0] * sx.x : sx.x; s[r][b][1] = Z ? z[r][0] * sx.y : sx.y;
+                    s[r][b][2] = Z ? z[r][1] * sx.x : sx.x; s[r][b][3] = Z ? z[r][1] * sx.y : sx.y;
+                }
+            }
+        }
+        uint4 x[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) x[b] = *reinterpret_cast<const uint4*>(xs + k * tile + at[b]);
+#pragma unroll
+        for (int r = 0; r < G4_NR; ++r) {
+            const uint32_t w0 = k & 1 ? st.w[r][k >> 1].z : st.w[r][k >> 1].x;
+            const uint32_t w1 = k & 1 ? st.w[r][k >> 1].w : st.w[r][k >> 1].y;
+            const uint32_t v0 = __byte_perm(w0, 0, 0x2301), v1 = __byte_perm(w1, 0, 0x2301);
+            const uint32_t a0[4] = {w0 & 0x00780078u, w1 & 0x00780078u, w0 & 0x07800780u, w1 & 0x07800780u};
+            const uint32_t a1[4] = {v0 & 0x00780078u, v1 & 0x00780078u, v0 & 0x07800780u, v1 & 0x07800780u};
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                g4_mma(s[r][b], a0, x[b].x, x[b].y, s[r][b]);
+                g4_mma(s[r][b], a1, x[b].z, x[b].w, s[r][b]);
+            }
+        }
+        if ((k + 1) * 32 % G == 0) {
+#pragma unroll
+            for (int r = 0; r < G4_NR; ++r) {
+                __half2 h;
+                memcpy(&h, &st.s[r][j], 4);
+                const float2 f = __half22float2(h);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[r][b][i] = fmaf(i < 2 ? f.x : f.y, s[r][b][i], acc[r][b][i]);
+            }
+        }
+    }
+    static_assert(NG >= 1, "a group is at most a chunk");
 }
 
 __device__ __forceinline__ float g4_silu_mul(float g, float u) {
     return g < -64.f ? silu_mul_tail(g, u) : g / (1.f + expf(-g)) * u;
 }
 
-// A unit is two row-groups against up to 8 rows of x: rows 32u .. 32u + 31 of
-// the matrix, or (PAIR) the gate and the up rows 16u .. 16u + 15.  A team of
-// p.team warps shares a unit, warp i of it the chunks i, i + team, ...; the
-// partial sums meet in shared memory and are added in warp order.
-template <int XT, int G, bool Z, bool PAIR>
-__global__ void __launch_bounds__(G4_THREADS, 1) g4_kernel(G4Params p) {
-    __shared__ float red[2][G4_WARPS][8][32];
-    __shared__ int32_t blk[G4_MAXE + 1];   // column blocks before expert e
-    __shared__ int32_t wsum[G4_WARPS];
+// Rows of x by expert, read once per CTA: blk[e] slots (passes of p.cols rows)
+// before expert e, and its rows lo[e] .. hi[e].
+struct G4Rows {
+    int32_t blk[G4_MAXE + 1];
+    int32_t lo[G4_MAXE];
+    int32_t hi[G4_MAXE];
+    int32_t wsum[32];
+};
+
+template <int WARPS>
+__device__ __forceinline__ int g4_rows(G4Rows& s, const G4Params& p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    grid_dep_launch();
-    grid_dep_wait();
-    int blocks = 1;
-    if (p.offsets) {
-        auto rows_of = [&](int e) {
-            if (e >= p.E) return 0;
-            const int lo = max(0, min(p.offsets[e], p.R)), hi = max(0, min(p.offsets[e + 1], p.R));
-            return max(0, hi - lo);
-        };
-        const int a = (rows_of(2 * tid) + 7) >> 3, b = (rows_of(2 * tid + 1) + 7) >> 3;
-        int s = a + b;
+    constexpr int PER = (G4_MAXE + 32 * WARPS - 1) / (32 * WARPS);
+    int n[PER], sum = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += v;
+    for (int i = 0; i < PER; ++i) {
+        const int e = PER * tid + i;
+        int lo = 0, hi = 0;
+        if (e < p.E) {
+            lo = max(0, min(p.offsets[e], p.R));
+            hi = max(lo, min(p.offsets[e + 1], p.R));
         }
-        if (lane == 31) wsum[warp] = s;
-        __syncthreads();
-        int before = 0;
-#pragma unroll
-        for (int w = 0; w < G4_WARPS; ++w) before += w < warp ? wsum[w] : 0;
-        blk[2 * tid] = before + s - a - b;
-        blk[2 * tid + 1] = before + s - b;
-        if (tid == G4_THREADS - 1) blk[G4_MAXE] = before + s;
-        __syncthreads();
-        blocks = blk[G4_MAXE];
+        if (e < G4_MAXE) {
+            s.lo[e] = lo;
+            s.hi[e] = hi;
+        }
+        n[i] = (hi - lo + p.cols - 1) / p.cols;
+        sum += n[i];
     }
-    const int team = warp / p.team, member = warp % p.team, teams = G4_WARPS / p.team;
-    const long long total = (long long)blocks * p.units;
-    const long long step = (long long)gridDim.x * teams;
-    const int rgs = (p.N + 15) / 16;
-    const int full = g4_chunk_bytes(G4_CHUNK, G, Z);
-    int par = 0;
-    for (long long u = (long long)blockIdx.x + (long long)team * gridDim.x; u < total; u += step) {
-        const int slot = (int)(u / p.units), unit = (int)(u % p.units);
-        int e = 0, row0 = 0, cols = p.R;
-        if (p.offsets) {
-            int lo = 0, hi = p.E;   // the largest e with blk[e] <= slot
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (blk[mid] <= slot) lo = mid;
-                else hi = mid;
-            }
-            e = lo;
-            row0 = max(0, min(p.offsets[e], p.R)) + 8 * (slot - blk[e]);
-            cols = min(8, max(0, min(p.offsets[e + 1], p.R)) - row0);
-        }
-        const uint8_t* r0;
-        const uint8_t* r1;
-        if constexpr (PAIR) {
-            r0 = p.W0 + e * p.stride + unit * p.rg_bytes;
-            r1 = p.W1 + e * p.stride + unit * p.rg_bytes;
-        } else {
-            r0 = p.W0 + e * p.stride + 2LL * unit * p.rg_bytes;
-            r1 = 2 * unit + 1 < rgs ? r0 + p.rg_bytes : r0;   // past the end: read again, dropped below
-        }
-        const int g = lane >> 2, t = lane & 3;
-        const bool live = g < cols;
-        const long long xrow = (long long)(row0 + g) * p.K + 8 * t;
-        float acc[2][4] = {};
-        for (int c = member; c < p.chunks; c += p.team) {
-            const int nc = min(G4_CHUNK, p.K - c * G4_CHUNK);
-            g4_chunk<XT, G, Z>(r0 + (long long)c * full, r1 + (long long)c * full, nc, p.x, xrow + c * G4_CHUNK, live,
-                               lane, acc);
-        }
+    const int own = sum;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) red[par][warp][i][lane] = acc[i >> 2][i & 3];
-        if (p.team > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * p.team) : "memory");
-        else __syncwarp();
-        constexpr int OUT = PAIR ? 128 : 256;
-        for (int o = member * 32 + lane; o < OUT; o += 32 * p.team) {
-            const int i = o >> 5, l = o & 31;
-            const int col = 2 * (l & 3) + (i & 1);
-            const int row = (PAIR ? 16 : 32) * unit + (i >> 2) * 16 + ((i & 2) ? 8 : 0) + (l >> 2);
-            if (col < cols && row < p.N) {
-                float a = 0.f, b = 0.f;
-                for (int w = 0; w < p.team; ++w) {
-                    a += red[par][team * p.team + w][i][l];
-                    if constexpr (PAIR) b += red[par][team * p.team + w][i + 4][l];
-                }
-                p.y[(long long)(row0 + col) * p.N + row] = PAIR ? g4_silu_mul(a, b) : a;
-            }
-        }
-        par ^= 1;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
     }
+    if (lane == 31) s.wsum[warp] = sum;
+    __syncthreads();
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) before += w < warp ? s.wsum[w] : 0;
+    int at = before + sum - own;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (PER * tid + i < G4_MAXE) s.blk[PER * tid + i] = at;
+        at += n[i];
+    }
+    if (tid == 32 * WARPS - 1) s.blk[G4_MAXE] = before + sum;
+    __syncthreads();
+    return s.blk[G4_MAXE];
 }
 
-// Warps per unit: the fewest rounds of chunks, and of equals the fewest warps
-// (less to add up).
-inline int g4_team(long long units, int chunks, int sms) {
-    int best = 1;
+// A value that is the same in all lanes, told to the compiler (it then lives in a
+// uniform register and its branches need no reconvergence).
+__device__ __forceinline__ int g4_uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// A unit: row-groups of a matrix against the columns of a slot (one pass over the
+// matrix of expert e).
+struct G4Walk {
+    int slot, unit, e;
+    // by all lanes of a warp, or (ONE) by one thread
+    template <bool ONE = false>
+    __device__ __forceinline__ void start(int u, const G4Rows* s, const G4Params& p) {
+        slot = u / p.units;
+        unit = u % p.units;
+        e = 0;
+        if (p.offsets) {    // the largest e with blk[e] <= slot
+            for (int hi = p.E; hi - e > 1;) {
+                const int mid = (e + hi) >> 1;
+                if (s->blk[mid] <= slot) e = mid;
+                else hi = mid;
+            }
+            if constexpr (!ONE) e = g4_uniform(e);
+        }
+    }
+    __device__ __forceinline__ void step(int by, const G4Rows* s, const G4Params& p) {
+        unit += by;
+        if (unit < p.units) return;
+        do {
+            unit -= p.units;
+            ++slot;
+        } while (unit >= p.units);
+        if (p.offsets) {
+            while (e + 1 < p.E && s->blk[e + 1] <= slot) ++e;
+            e = g4_uniform(e);
+        }
+    }
+    __device__ __forceinline__ int row(const G4Rows* s, const G4Params& p) const {
+        return p.offsets ? s->lo[e] + p.cols * (slot - s->blk[e]) : 0;
+    }
+    __device__ __forceinline__ int cols(const G4Rows* s, const G4Params& p, int row) const {
+        return min(p.cols, (p.offsets ? s->hi[e] : p.R) - row);
+    }
+};
+
+// The x that is in shared memory: the columns of slots first .. end - 1.
+constexpr int G4_COLS = 32;
+struct G4Phase {
+    int first, end, cols, products;
+    int row[G4_COLS];                // of a column: its row of x, the place of its (first) sum
+    int sum[G4_COLS];
+    uint32_t top[G4_COLS];           // largest |x|, as fp32 bits
+    float down[G4_COLS];             // 2^-E (NaN for a column with an infinity or a NaN)
+    int slot_col[G4_COLS], slot_prod[G4_COLS];   // of a slot: its first column and product
+};
+
+// As many slots from f on as there is room for, up to the one of the CTA's last
+// unit.  One thread.
+template <int XT, int G>
+__device__ void g4_plan(G4Phase& ph, G4Walk f, int last_slot, const G4Rows* s, const G4Params& p) {
+    constexpr int P = G4X<XT>::PARTS, CO = G4X<XT>::COLS;
+    ph.first = f.slot;
+    int cols = 0, products = 0, n = 0;
+    for (;;) {
+        const int row = f.row(s, p), c = f.cols(s, p, row), q = (c + CO - 1) / CO;
+        if (n && (cols + c > G4_COLS ||
+                  (p.c1 - p.c0) * g4_x_bytes(G, products + q + 1, (cols + c) * P) > p.x_room))
+            break;
+        ph.slot_col[n] = cols;
+        ph.slot_prod[n] = products;
+        for (int j = 0; j < c; ++j) {
+            ph.row[cols + j] = row + j;
+            ph.sum[cols + j] = (products + j / CO) * 8 + j % CO * (8 / CO);
+            ph.top[cols + j] = 0;
+        }
+        cols += c;
+        products += q;
+        ++n;
+        if (f.slot == last_slot || cols == G4_COLS) break;
+        ++f.slot;
+        while (f.e + 1 < p.E && s->blk[f.e + 1] <= f.slot) ++f.e;
+    }
+    ph.end = ph.first + n;
+    ph.cols = cols;
+    ph.products = products + 1;      // a second product may be read where a slot has only one
+}
+
+// x of the planned columns into shared memory, by all warps.
+template <int XT, int G, bool Z>
+__device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, uint8_t* xs) {
+    constexpr int P = G4X<XT>::PARTS, XB = G4X<XT>::BYTES, WARPS = G4X<XT>::WARPS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int chunks = p.c1 - p.c0, tile = ph.cols * P * 64, items = ph.cols * chunks;
+    const int x_chunk = g4_x_bytes(G, ph.products, ph.cols * P);
+    auto load = [&](int col, int c, float v[4]) {
+        const int k = (p.c0 + c) * G4_CHUNK + 4 * lane;
+        v[0] = v[1] = v[2] = v[3] = 0.f;
+        if (k < p.K) g4_load_x<XT>((const uint8_t*)p.x + ((long long)ph.row[col] * p.K + k) * XB, v);
+    };
+    for (int i = warp; i < items; i += WARPS) {
+        const int col = i / chunks;
+        float v[4];
+        load(col, i - col * chunks, v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0 && m) atomicMax(&ph.top[col], m);
+    }
+    __syncthreads();
+    for (int i = warp; i < items; i += WARPS) {
+        const int col = i / chunks, c = i - col * chunks;
+        float v[4];
+        load(col, c, v);
+        const uint32_t top = ph.top[col];
+        // the largest lands in [2^13, 2^14); at most 2^126, which still keeps the smallest columns whole
+        const int E = min(126, 13 + 127 - (int)(top >> 23));
+        const float up = __uint_as_float((uint32_t)(127 + E) << 23);
+        if (c == 0 && lane == 0)
+            ph.down[col] = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : (uint32_t)(127 - E) << 23);
+        // k = 32 (lane / 8) + 4 (lane % 8): columns 8t + 0, 1 (times 1) and 8t + 2, 3 (by 16), or + 4, 5 and + 6, 7
+        v[0] *= up; v[1] *= up;
+        v[2] *= up * 0.0625f; v[3] *= up * 0.0625f;
+        uint8_t* at = xs + c * x_chunk;
+        uint8_t* bytes = at + (lane >> 3) * tile + col * (P * 64) + (lane & 7) * 8;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+            uint2 o;
+            memcpy(&o.x, &a, 4);
+            memcpy(&o.y, &b, 4);
+            *reinterpret_cast<uint2*>(bytes + q * 64) = o;
+            const float2 f = __half22float2(a), h = __half22float2(b);
+            v[0] = (v[0] - f.x) * 2048.f; v[1] = (v[1] - f.y) * 2048.f;
+            v[2] = (v[2] - h.x) * 2048.f; v[3] = (v[3] - h.y) * 2048.f;
+            float s = fmaf(h.x + h.y, 16.f, f.x + f.y);
+#pragma unroll
+            for (int d = 1; d < G / 4; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            if (lane % (G / 4) == 0)
+                reinterpret_cast<float*>(at + 4 * tile)[lane / (G / 4) * ph.products * 8 + ph.sum[col] + q] =
+                    s * (Z ? -0x1.0p-21f : -0x1.0p-18f);
+        }
+    }
+    __syncthreads();
+}
+
+// A unit is two row-groups against up to p.cols rows of x: rows 32u .. 32u + 31
+// of the matrix, or (PAIR) the gate and the up rows 16u .. 16u + 15.  A CTA takes a
+// contiguous range of all units (so that it meets few slots), its teams of p.team warps
+// the units of the range in turn; warp i of a team takes the chunks i, i + team, ...
+//
+// Every warp streams its own chunks through its own ring of two stages in shared
+// memory (cp.async), across the ends of units.  The partial sums meet in shared memory
+// and are added in warp order.  That is put off until the team's buffer is full (8 units
+// of one column, 1 of 8), so that the warps of a team wait for one another as rarely
+// as they can.
+template <int XT, int G, bool Z, bool PAIR>
+__global__ void __launch_bounds__(G4X<XT>::WARPS * 32, 1) g4_kernel(G4Params p) {
+    constexpr int FULL = g4_chunk_bytes(G4_CHUNK, G, Z);
+    constexpr int P = G4X<XT>::PARTS, WARPS = G4X<XT>::WARPS;
+    constexpr int STAGE = G4_NR * FULL, RING = 2 * STAGE;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int2 wait_all[WARPS][8];   // (unit, row of y) of the blocks of 32 sums that wait
+    __shared__ G4Phase ph;
+    // shared memory: sums, rings, x, rows by expert
+    float* const red_all = reinterpret_cast<float*>(smem);
+    uint8_t* const xs = smem + WARPS * 1024 + WARPS * RING;
+    G4Rows* const rows = reinterpret_cast<G4Rows*>(xs + p.x_room);
+    const int lane = threadIdx.x & 31, warp = g4_uniform(threadIdx.x >> 5);
+    const int team = warp / p.team, member = warp % p.team, teams = WARPS / p.team;
+    float* const red = red_all + team * p.team * 256;
+    const int chunks = p.c1 - p.c0;
+    grid_dep_launch();
+    grid_dep_wait();
+    const int slots = p.offsets ? g4_uniform(g4_rows<WARPS>(*rows, p)) : 1;
+    const int total = slots * p.units;
+    const int u0 = (int)((long long)total * blockIdx.x / gridDim.x), u1 = (int)((long long)total * (blockIdx.x + 1) / gridDim.x);
+    if (u0 == u1) return;
+
+    // loads: the next chunk of this warp, in order
+    G4Walk w;
+    w.start(min(u0 + team, total - 1), rows, p);
+    const uint8_t* const ring = smem + WARPS * 1024 + warp * RING;
+    const uint32_t ring_s = smem_u32(ring) + lane * 16;
+    const int o_tail = (lane >> 4) * (FULL - 256) + 1024;              // the lane's piece behind the codes of either row-group
+    const bool has_tail = (lane & 15) * 16 < FULL - 1024;
+    // the warp's chunks of a unit; the last of them may be the short end of K
+    const int n = g4_uniform((chunks - member + p.team - 1) / p.team);
+    const int last = p.K - (p.c0 + member + (n - 1) * p.team) * G4_CHUNK;
+    const int end = last < G4_CHUNK ? 1 : 0;                           // chunks to go when the short one is next, 0: there is none
+    const int jump = p.team * FULL;
+    int left = u0 + team < u1 ? (u1 - u0 - team + teams - 1) / teams : 0;   // units of this team
+    int fu = left, fl = left ? n : 0, fstage = 0;                      // units, chunks of the unit still to load
+    const uint8_t *f0 = nullptr, *f1 = nullptr, *f2 = nullptr;         // the lane's pieces: codes of both, and behind
+    G4Walk f = w;
+    auto aim = [&]() {
+        const long long at = f.e * p.stride + (long long)(p.c0 + member) * FULL;
+        const uint8_t *r0, *r1;
+        if constexpr (PAIR) {
+            r0 = p.W0 + at + f.unit * p.rg_bytes;
+            r1 = p.W1 + at + f.unit * p.rg_bytes;
+        } else {
+            r0 = p.W0 + at + 2LL * f.unit * p.rg_bytes;
+            r1 = 2 * f.unit + 1 < (p.N + 15) / 16 ? r0 + p.rg_bytes : r0;   // past the end: read again, dropped below
+        }
+        f0 = r0 + lane * 16;
+        f1 = r1 + lane * 16;
+        f2 = (lane >> 4 ? r1 : r0) + 1024 + (lane & 15) * 16;
+    };
+    auto fetch = [&]() {
+        if (fl) {
+            const uint32_t d = ring_s + fstage;
+            if (fl != end) {
+                g4_cp16(d, f0);
+                g4_cp16(d + 512, f0 + 512);
+                g4_cp16(d + FULL, f1);
+                g4_cp16(d + FULL + 512, f1 + 512);
+                if (has_tail) g4_cp16(d + o_tail, f2);
+            } else {
+                const int bytes = g4_chunk_bytes(last, G, Z) - lane * 16;
+                for (int i = 0; i < bytes; i += 512) {
+                    g4_cp16(d + i, f0 + i);
+                    g4_cp16(d + FULL + i, f1 + i);
+                }
+            }
+            f0 += jump;
+            f1 += jump;
+            f2 += jump;
+            if (--fl == 0 && --fu > 0) {
+                f.step(teams, rows, p);
+                fl = n;
+                aim();
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        fstage ^= STAGE;
+    };
+    if (fl) aim();
+    fetch();
+    fetch();
+
+    const int g = lane >> 2, t = lane & 3;
+    int used = 0, stage = 0;   // used: blocks of 32 sums in the buffer
+    auto meet = [&]() {
+        if (p.team > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * p.team) : "memory");
+        else __syncwarp();
+    };
+    // add up what waits in the team's buffer, a block of 32 sums per warp and turn
+    auto flush = [&]() {
+        meet();
+        for (int i = member; i < used; i += p.team) {
+            const int2 q = wait_all[team][i];
+            float a = 0.f;
+            for (int m = 0; m < p.team; ++m) a += red[(i * p.team + m) * 32 + lane];
+            int row = (PAIR ? 16 : 32) * q.x + lane;
+            if constexpr (PAIR) {
+                const float b = __shfl_down_sync(0xffffffffu, a, 16);
+                a = g4_silu_mul(a, b);
+                if (lane >= 16) row = p.N;
+            }
+            if (row < p.N) {
+                float* out = p.y + (long long)q.y * p.N + row;
+                *out = p.c0 ? *out + a : a;
+            }
+        }
+        meet();   // the buffer is written again
+        used = 0;
+    };
+    int phase_end = -1, first = 0, tile = 0, x_chunk = 0, products = 0;
+    // one unit with NB products
+    auto unit = [&](auto nb, int cols, int col0, int prod0) {
+        constexpr int NB = decltype(nb)::value;
+        float acc[G4_NR][NB][4] = {};
+        int at[NB];   // the row of x that the lane multiplies with (there may be fewer: the last one, and not counted)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            at[b] = (P == 1 ? col0 + min(g, cols - 1) : (col0 + min(2 * b + (g >> 2), cols - 1)) * 3 + min(g & 3, 2)) * 64 + t * 16;
+        const uint8_t* xc = xs + member * x_chunk;
+        const int xjump = p.team * x_chunk;
+        const int sum0 = 4 * tile + prod0 * 32 + 8 * t, sum_step = products * 32;
+#pragma unroll 1
+        for (int i = n; i > 0; --i) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncwarp();   // the scales and zeros came by other lanes' copies
+            G4Stage<G, Z> st;
+            st.load(ring + stage, i != end ? G4_CHUNK : last, lane);
+            g4_chunk<G, Z, NB>(st, xc, at, tile, xc + sum0, sum_step, acc);
+            xc += xjump;
+            __syncwarp();   // every lane has read the stage
+            fetch();
+            stage ^= STAGE;
+        }
+        // sums are 2^-21 of theirs, part q of a column 2^(-21 - 11q)
+        float* const mine = red + (used * p.team + member) * 32 + g;
+        const float* const down = ph.down + col0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < (P == 1 ? 2 : 1); ++i) {
+                const int col = P == 1 ? 2 * t + i : 2 * b + (t >> 1);
+                const float dn = down[min(col, cols - 1)];
+#pragma unroll
+                for (int r = 0; r < G4_NR; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float v = acc[r][b][2 * h + i] * 0x1.0p21f;
+                        if constexpr (P > 1) {
+                            v = t & 1 ? v * 0x1.0p-22f : fmaf(acc[r][b][2 * h + 1], 0x1.0p10f, v);
+                            v += __shfl_xor_sync(0xffffffffu, v, 1);
+                        }
+                        if (col < cols && (P == 1 || !(t & 1))) mine[col * p.team * 32 + 16 * r + 8 * h] = v * dn;
+                    }
+            }
+    };
+    for (int u = u0 + team;; ) {
+        // x of the next slots, when the CTA is through with the last ones
+        if (threadIdx.x == 0) {
+            G4Walk q = w;
+            q.start<true>(phase_end < 0 ? u0 : phase_end * p.units, rows, p);
+            g4_plan<XT, G>(ph, q, (u1 - 1) / p.units, rows, p);
+        }
+        __syncthreads();
+        first = ph.first;
+        phase_end = g4_uniform(ph.end);
+        products = g4_uniform(ph.products);
+        tile = g4_uniform(ph.cols) * P * 64;
+        x_chunk = g4_x_bytes(G, products, g4_uniform(ph.cols) * P);
+        g4_stage_x<XT, G, Z>(p, ph, xs);
+        for (; u < u1 && w.slot < phase_end; u += teams) {
+            const int row0 = g4_uniform(w.row(rows, p)), cols = g4_uniform(w.cols(rows, p, row0));
+            const int col0 = g4_uniform(ph.slot_col[w.slot - first]), prod0 = g4_uniform(ph.slot_prod[w.slot - first]);
+            if (used + cols > 8) flush();
+            if (P == 1 || cols <= 2) unit(std::integral_constant<int, 1>(), cols, col0, prod0);
+            else unit(std::integral_constant<int, P == 1 ? 1 : 2>(), cols, col0, prod0);
+            if (member == 0 && lane < cols) wait_all[team][used + lane] = make_int2(w.unit, row0 + lane);
+            used += cols;
+            w.step(teams, rows, p);
+        }
+        if (phase_end * (long long)p.units >= u1) break;
+        __syncthreads();   // x is written again
+    }
+    if (used) flush();
+}
+
+// Warps per unit: the least time of the busiest team, a unit costing its chunks and
+// about one chunk more (walking, adding up).
+inline int g4_team(long long units, int chunks, int sms, int warps) {
+    int best = warps;
     long long cost = -1;
-    for (int s = 1; s <= G4_WARPS; s *= 2) {
-        if (s > 1 && s > chunks) break;
-        const long long teams = (long long)sms * (G4_WARPS / s);
-        const long long c = (units + teams - 1) / teams * ((chunks + s - 1) / s);
+    for (int s = warps; s >= 1; --s) {
+        if (warps % s || (s > 1 && warps / s > 15)) continue;   // a named barrier per team
+        const long long teams = (long long)sms * (warps / s);
+        const long long c = (units + teams - 1) / teams * ((chunks + s - 1) / s + 1);
         if (cost < 0 || c < cost) {
             cost = c;
             best = s;
@@ -283,30 +625,65 @@ inline int g4_team(long long units, int chunks, int sms) {
     return best;
 }
 
-template <int XT, int G, bool Z>
-cudaError_t g4_launch_t(G4Params p, cudaStream_t stream) {
+template <int XT, int G, bool Z, bool PAIR>
+cudaError_t g4_launch_p(G4Params p, cudaStream_t stream) {
     int sms = 0;
     cudaError_t e = device_sms(sms);
     if (e != cudaSuccess) return e;
+    constexpr int P = G4X<XT>::PARTS, CO = G4X<XT>::COLS, WARPS = G4X<XT>::WARPS;
+    constexpr int FULL = g4_chunk_bytes(G4_CHUNK, G, Z);
+    const int fixed = WARPS * 1024 + WARPS * 2 * G4_NR * FULL + (p.offsets ? (int)sizeof(G4Rows) : 0);
+    const int room = (G4_SMEM - (int)sizeof(G4Phase) - WARPS * 64 - 512 - fixed) & ~127;   // less the kernel's static part
     p.rg_bytes = g4_rowgroup_bytes(p.K, G, Z);
-    p.chunks = (p.K + G4_CHUNK - 1) / G4_CHUNK;
-    p.units = p.W1 ? (p.N + 15) / 16 : (p.N + 31) / 32;
-    const long long units = (long long)p.units * (p.offsets ? std::min(p.E, p.R) : 1);
-    p.team = g4_team(units, p.chunks, sms);
-    // at most one column block per row, so never more units than this
-    const long long most = (long long)p.units * (p.offsets ? p.R : 1);
-    const int grid = (int)std::min<long long>(sms, most);
-    return p.W1 ? launch_dependent(g4_kernel<XT, G, Z, true>, grid, G4_THREADS, 0, stream, p)
-                : launch_dependent(g4_kernel<XT, G, Z, false>, grid, G4_THREADS, 0, stream, p);
+    p.units = PAIR ? (p.N + 15) / 16 : (p.N + 31) / 32;
+    const int chunks = (p.K + G4_CHUNK - 1) / G4_CHUNK;
+    // columns of a pass: as many as there can be, up to 8 (fp32 x: 4, two products), with the x of all of K
+    // in shared memory.  Where that does not fit, fewer columns a pass (gate/up, whose sums have to be
+    // whole before silu) or K in parts, one launch each (the weights are then still read once).
+    p.cols = std::min(p.R, P == 1 ? 8 : 4);
+    int span = 0, x_chunk = 0;
+    while (true) {
+        x_chunk = g4_x_bytes(G, (p.cols + CO - 1) / CO + 1, p.cols * P);
+        span = std::min(chunks, room / x_chunk);
+        if (span == chunks || !PAIR || p.cols == 1) break;
+        --p.cols;
+    }
+    if (span < 1 || (PAIR && span < chunks)) return cudaErrorNotSupported;
+    // one matrix has one slot; experts up to one per row, and room for several
+    p.x_room = p.offsets ? room : span * x_chunk;
+    p.team = g4_team((long long)p.units * (p.offsets ? std::min(p.E, p.R) : 1), span, sms, WARPS);
+    const long long total = (long long)p.units * (p.offsets ? p.R : 1);
+    const int grid = (int)std::min<long long>(sms, total);
+    const int smem = fixed + p.x_room;
+    auto kernel = g4_kernel<XT, G, Z, PAIR>;
+    static SmemLimit limit;   // one per instantiation
+    e = limit.ensure((const void*)kernel, smem);
+    const int all = p.R;
+    for (int r = 0; r < all && e == cudaSuccess; r += p.R) {
+        if (!p.offsets) {   // one matrix: a launch serves p.cols columns
+            p.R = std::min(p.cols, all - r);
+            p.x = (const uint8_t*)p.x + (r ? (long long)p.cols * p.K * G4X<XT>::BYTES : 0);
+            p.y += r ? (long long)p.cols * p.N : 0;
+        }
+        for (p.c0 = 0; p.c0 < chunks && e == cudaSuccess; p.c0 = p.c1) {
+            p.c1 = std::min(chunks, p.c0 + span);
+            e = launch_dependent(kernel, grid, WARPS * 32, smem, stream, p);
+        }
+    }
+    return e;
+}
+
+template <int XT, int G>
+cudaError_t g4_launch_g(const G4Params& p, bool zeros, cudaStream_t stream) {
+    if (p.W1) return zeros ? g4_launch_p<XT, G, true, true>(p, stream) : g4_launch_p<XT, G, false, true>(p, stream);
+    return zeros ? g4_launch_p<XT, G, true, false>(p, stream) : g4_launch_p<XT, G, false, false>(p, stream);
 }
 
 template <int XT>
 cudaError_t g4_launch_x(const G4Params& p, int G, bool zeros, cudaStream_t stream) {
-    switch (G) {
-        case 32: return zeros ? g4_launch_t<XT, 32, true>(p, stream) : g4_launch_t<XT, 32, false>(p, stream);
-        case 64: return zeros ? g4_launch_t<XT, 64, true>(p, stream) : g4_launch_t<XT, 64, false>(p, stream);
-        default: return zeros ? g4_launch_t<XT, 128, true>(p, stream) : g4_launch_t<XT, 128, false>(p, stream);
-    }
+    return G == 32   ? g4_launch_g<XT, 32>(p, zeros, stream)
+           : G == 64 ? g4_launch_g<XT, 64>(p, zeros, stream)
+                     : g4_launch_g<XT, 128>(p, zeros, stream);
 }
 
 }  // namespace

@@ -10,14 +10,17 @@ struct G4Params {
     const uint8_t* W0;        // packed matrix, or the experts' matrices at a stride (gate of gate/up)
     const uint8_t* W1;        // up matrices of gate/up, else null
     long long stride;         // bytes between experts
-    const int32_t* offsets;   // [E + 1] rows of x by expert, or null: one matrix, R <= 8 rows
+    const int32_t* offsets;   // [E + 1] rows of x by expert, or null: one matrix for all R rows
     int E, R, N, K;
     const void* x;            // [R][K]
     float* y;                 // [R][N]
+    // set by the launcher
     long long rg_bytes;       // bytes of a row-group
-    int chunks;               // chunks of a row-group
+    int c0, c1;               // chunks of this launch; c0 > 0 adds to y
     int units;                // units of a matrix
     int team;                 // warps that share a unit
+    int cols;                 // rows of x per pass over a matrix, at most
+    int x_room;               // shared memory for x
 };
 
 // x_dtype: 0 bf16, 1 fp32, 2 fp16

@@ -3,24 +3,24 @@
 // W[n][c] = scale[n][c / G] * (code[n][c] - zero[n][c / G]), codes and zeros
 // 0..15, binary16 scales, G = 32, 64 or 128 columns a group, cols % G == 0.
 // Rows are padded to row-groups of 16; a row-group is one contiguous stream of
-// chunks of 256 columns (the last one may be shorter).  A chunk of nc columns:
+// chunks of 128 columns (the last one may be shorter).  A chunk of nc columns:
 //   codes   ceil(nc / 64) slabs of 512 bytes; a slab holds two 32-column tiles,
 //           lane L = 4g + t at L * 16: words [tile 0 row g][tile 0 row g + 8]
-//           [tile 1 row g][tile 1 row g + 8]; nibble i (i < 4) of a word is the
-//           code of column 8t + 2i of its tile, nibble 4 + i that of 8t + 2i + 1
-//   scales  per group 8 words, word g = (row g, row g + 8)
-//   zeros   (if any) per group 8 bytes, byte g = row g | row g + 8 << 4; padded
-//           to 16 bytes
+//           [tile 1 row g][tile 1 row g + 8]; half j (0, 1) of a word is
+//           c0 | c1 << 4 | c2 << 8 | c3 << 12 turned left by 3 bits, ci the
+//           code of column 8t + 2i + j of its tile
+//   scales  [g][group] words: row g | row g + 8 << 16
+//   zeros   (if any) [g][group] bytes: row g | row g + 8 << 4; padded to 16 bytes
 // so that lane L's 16 bytes of a slab are its A operands of four m16n8k16
 // products, and every section starts on a 16-byte boundary.
 #pragma once
 #include <stddef.h>
 #include <stdint.h>
 
-#define G4_CHUNK 256
+#define G4_CHUNK 128
 
 #ifdef __CUDACC__
-#define G4_HD __host__ __device__ __forceinline__
+#define G4_HD __host__ __device__ __forceinline__ constexpr
 #else
 #define G4_HD static inline
 #endif

@@ -14,11 +14,11 @@ namespace rfx {
 namespace {
 
 // Word of lane quarter t for 8 codes (columns 8t .. 8t + 7, low nibbles of b).
-G4_HD uint32_t g4_word(const uint8_t b[8]) {
+__host__ __device__ __forceinline__ uint32_t g4_word(const uint8_t b[8]) {
     uint32_t w = 0;
-    for (int i = 0; i < 4; ++i) {
-        w |= (uint32_t)(b[2 * i] & 15u) << (4 * i);
-        w |= (uint32_t)(b[2 * i + 1] & 15u) << (16 + 4 * i);
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t h = (b[j] & 15u) | (b[2 + j] & 15u) << 4 | (b[4 + j] & 15u) << 8 | (b[6 + j] & 15u) << 12;
+        w |= ((h << 3 | h >> 13) & 0xFFFFu) << (16 * j);
     }
     return w;
 }
@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(256) g4_pack_kernel(const uint8_t* __restrict_
         const int groups = nc / G;
         const long long g0 = (long long)c * G4_CHUNK / G;
         for (int j = lane; j < groups * 8; j += 32) {
-            const long long r0 = rg * 16 + (j & 7), r1 = r0 + 8;
-            const long long at = g0 + (j >> 3);
+            const long long r0 = rg * 16 + j / groups, r1 = r0 + 8;
+            const long long at = g0 + j % groups;
             const uint32_t s0 = r0 < rows ? scales[r0 * ng + at] : 0u, s1 = r1 < rows ? scales[r1 * ng + at] : 0u;
             *reinterpret_cast<uint32_t*>(out + g4_scale_off(nc) + j * 4) = s0 | s1 << 16;
         }
@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(256) g4_pack_kernel(const uint8_t* __restrict_
             for (int j = lane; j < bytes; j += 32) {
                 uint32_t v = 0;
                 if (j < groups * 8) {
-                    const long long r0 = rg * 16 + (j & 7), r1 = r0 + 8;
-                    const long long at = g0 + (j >> 3);
+                    const long long r0 = rg * 16 + j / groups, r1 = r0 + 8;
+                    const long long at = g0 + j % groups;
                     if (r0 < rows) v |= zeros[r0 * ng + at] & 15u;
                     if (r1 < rows) v |= (zeros[r1 * ng + at] & 15u) << 4;
                 }
@@ -129,10 +129,10 @@ void g4_pack_host(const uint8_t* codes, const uint16_t* scales, const uint8_t* z
             for (int j = 0; j < nc / G; ++j)
                 for (int i = 0; i < 16 && rg * 16 + i < rows; ++i) {
                     const int64_t at = (rg * 16 + i) * ng + k0 / G + j;
-                    uint8_t* d = out + g4_scale_off(nc) + (j * 8 + (i & 7)) * 4 + (i >> 3) * 2;
+                    uint8_t* d = out + g4_scale_off(nc) + ((i & 7) * (nc / G) + j) * 4 + (i >> 3) * 2;
                     d[0] = (uint8_t)scales[at];
                     d[1] = (uint8_t)(scales[at] >> 8);
-                    if (zeros) out[g4_zero_off(nc, G) + j * 8 + (i & 7)] |= (uint8_t)(zeros[at] << (i >> 3) * 4);
+                    if (zeros) out[g4_zero_off(nc, G) + (i & 7) * (nc / G) + j] |= (uint8_t)(zeros[at] << (i >> 3) * 4);
                 }
             out += g4_chunk_bytes(nc, G, zeros != nullptr);
         }
@@ -150,14 +150,14 @@ void g4_unpack_host(const uint8_t* src, int64_t rows, int64_t cols, int G, uint8
             const int nc = (int)std::min<int64_t>(G4_CHUNK, cols - k0);
             for (int k = 0; k < nc; ++k) {
                 const uint8_t* s = in + k / 64 * 512 + (4 * g + (k / 8 & 3)) * 16 + ((k / 32 & 1) * 2 + h) * 4;
-                const int nib = (k & 7) / 2 + (k & 1) * 4;
-                codes[r * cols + k0 + k] = (uint8_t)(s[nib / 2] >> (nib & 1) * 4 & 15);
+                const uint32_t half = s[2 * (k & 1)] | (uint32_t)s[2 * (k & 1) + 1] << 8;
+                codes[r * cols + k0 + k] = (uint8_t)((half >> 3 | half << 13) >> (k & 6) * 2 & 15);
             }
             for (int j = 0; j < nc / G; ++j) {
-                const uint8_t* s = in + g4_scale_off(nc) + (j * 8 + g) * 4 + h * 2;
+                const uint8_t* s = in + g4_scale_off(nc) + (g * (nc / G) + j) * 4 + h * 2;
                 const int64_t at = r * ng + k0 / G + j;
                 scales[at] = (uint16_t)(s[0] | s[1] << 8);
-                if (zeros) zeros[at] = (uint8_t)(in[g4_zero_off(nc, G) + j * 8 + g] >> h * 4 & 15);
+                if (zeros) zeros[at] = (uint8_t)(in[g4_zero_off(nc, G) + g * (nc / G) + j] >> h * 4 & 15);
             }
             in += g4_chunk_bytes(nc, G, zeros != nullptr);
         }

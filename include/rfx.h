@@ -280,16 +280,18 @@ int rfx_gemv_q(rfx_format f, const void* W, int64_t N, int64_t K, const void* x,
  * 0.125 / 0.0625 more with zeros.
  *
  * Packed layout: rows padded to row-groups of 16 with zero codes and scales,
- * each row-group a contiguous stream of chunks of 256 columns (the last one
- * cols % 256).  A chunk of nc columns holds
+ * each row-group a contiguous stream of chunks of 128 columns (the last one
+ * cols % 128).  A chunk of nc columns holds
  *   codes:  ceil(nc / 64) slabs of 512 bytes, two 32-column tiles each; lane
  *           L = 4g + t (g = 0..7, t = 0..3) owns bytes 16L .. 16L + 15 of a slab,
  *           four little-endian words: (tile 0, row g), (tile 0, row g + 8),
- *           (tile 1, row g), (tile 1, row g + 8).  Nibble i = 0..3 of a word
- *           (bits 4i .. 4i + 3) is the code of column 8t + 2i of the tile, nibble
- *           4 + i the code of column 8t + 2i + 1.  A missing tile 1 is zero.
- *   scales: [nc / G][8] words, word g = scale of row g | scale of row g + 8 << 16
- *   zeros:  (has_zeros) [nc / G][8] bytes, byte g = zero of row g | zero of row
+ *           (tile 1, row g), (tile 1, row g + 8).  Half j = 0, 1 of a word (bits
+ *           16j .. 16j + 15) is c0 | c1 << 4 | c2 << 8 | c3 << 12 turned left by
+ *           3 bits, ci the code of column 8t + 2i + j of the tile.  A missing
+ *           tile 1 is zero.
+ *   scales: [8][nc / G] words, word (g, j) = scale of row g | scale of row g + 8 << 16
+ *           of the chunk's group j
+ *   zeros:  (has_zeros) [8][nc / G] bytes, byte (g, j) = zero of row g | zero of row
  *           g + 8 << 4, padded with zero bytes to a multiple of 16
  */
 

@@ -43,27 +43,30 @@ def test_layout_matches_header_description(rows, cols, G, zeros):
         return int(a[r, k]) if r < rows and k < a.shape[1] else 0
 
     for rg in range((rows + 15) // 16):
-        for k0 in range(0, cols, 256):
-            nc = min(256, cols - k0)
+        for k0 in range(0, cols, 128):
+            nc = min(128, cols - k0)
             for p in range((nc + 63) // 64):
                 for L in range(32):
                     g, t = L >> 2, L & 3
                     for tile in (0, 1):
                         for row in (16 * rg + g, 16 * rg + g + 8):
                             word = 0
-                            for i in range(4):
-                                k = p * 64 + tile * 32 + 8 * t + 2 * i
-                                if k < nc:
-                                    word |= at(c, row, k0 + k) << (4 * i) | at(c, row, k0 + k + 1) << (16 + 4 * i)
+                            for j in (0, 1):
+                                half = 0
+                                for i in range(4):
+                                    k = p * 64 + tile * 32 + 8 * t + 2 * i + j
+                                    if k < nc:
+                                        half |= at(c, row, k0 + k) << (4 * i)
+                                word |= ((half << 3 | half >> 13) & 0xFFFF) << (16 * j)
                             want += word.to_bytes(4, "little")
-            for j in range(nc // G):
-                for g in range(8):
+            for g in range(8):
+                for j in range(nc // G):
                     word = at(sb, 16 * rg + g, k0 // G + j) | at(sb, 16 * rg + g + 8, k0 // G + j) << 16
                     want += word.to_bytes(4, "little")
             if zeros:
                 part = bytearray()
-                for j in range(nc // G):
-                    for g in range(8):
+                for g in range(8):
+                    for j in range(nc // G):
                         part.append(at(z, 16 * rg + g, k0 // G + j) | at(z, 16 * rg + g + 8, k0 // G + j) << 4)
                 part += bytes(-len(part) % 16)
                 want += part
@@ -71,9 +74,9 @@ def test_layout_matches_header_description(rows, cols, G, zeros):
 
 
 def test_packed_bytes():
-    # per 256 columns and 16 rows: 2048 of codes, 32 of scales and 8 of zeros a group
-    assert rfx.rfx_g4_packed_bytes(4096, 4096, 128) == 256 * 16 * (2048 + 64)
-    assert rfx.rfx_g4_packed_bytes(17, 256, 32, True) == 2 * (2048 + 256 + 64)
+    # per 128 columns and 16 rows: 1024 of codes, 32 of scales and 8 of zeros (padded to 16) a group
+    assert rfx.rfx_g4_packed_bytes(4096, 4096, 128) == 256 * 32 * (1024 + 32)
+    assert rfx.rfx_g4_packed_bytes(17, 256, 32, True) == 2 * 2 * (1024 + 128 + 32)
     assert rfx.rfx_g4_packed_bytes(16, 128, 128, True) == 1024 + 32 + 16
     for rows, cols, G in ((16, 256, 16), (16, 200, 32), (16, 64, 128), (-1, 64, 64), (2 ** 31, 64, 64), (16, 0, 32)):
         assert rfx.rfx_g4_packed_bytes(rows, cols, G) == 0
