@@ -45,8 +45,9 @@ template <int XT> struct G4X {
     static constexpr int PARTS = XT == 1 ? 3 : 1;
     static constexpr int COLS = XT == 1 ? 2 : 8;
     static constexpr int BYTES = XT == 1 ? 4 : 2;
-    static constexpr int WARPS = XT == 1 ? 16 : 24;
 };
+// Warps of a CTA, by the products a pass may take: registers for two leave room for 16.
+constexpr int g4_warps(int nb) { return nb == 2 ? 16 : 24; }
 __host__ __device__ constexpr int g4_x_bytes(int G, int products, int rows) {
     return rows * (G4_CHUNK * 2) + G4_CHUNK / G * products * 32;
 }
@@ -215,55 +216,71 @@ __device__ __forceinline__ float g4_silu_mul(float g, float u) {
     return g < -64.f ? silu_mul_tail(g, u) : g / (1.f + expf(-g)) * u;
 }
 
-// Rows of x by expert, read once per CTA: blk[e] slots (passes of p.cols rows)
-// before expert e, and its rows lo[e] .. hi[e].
+// The experts with rows, read once per CTA: the i-th is expert e[i] with rows lo[i] ..
+// hi[i] and blk[i] slots (passes of p.cols rows) before it.
 struct G4Rows {
     int32_t blk[G4_MAXE + 1];
-    int32_t lo[G4_MAXE];
-    int32_t hi[G4_MAXE];
-    int32_t wsum[32];
+    int32_t e[G4_MAXE], lo[G4_MAXE], hi[G4_MAXE];
+    int32_t count;
+    int2 wsum[32];
 };
 
 template <int WARPS>
 __device__ __forceinline__ int g4_rows(G4Rows& s, const G4Params& p) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int PER = (G4_MAXE + 32 * WARPS - 1) / (32 * WARPS);
-    int n[PER], sum = 0;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int lo[PER], hi[PER], n[PER];
+    int2 sum = {0, 0};   // experts, slots
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = PER * tid + i;
-        int lo = 0, hi = 0;
+        lo[i] = hi[i] = 0;
         if (e < p.E) {
-            lo = max(0, min(p.offsets[e], p.R));
-            hi = max(lo, min(p.offsets[e + 1], p.R));
+            lo[i] = max(0, min(p.offsets[e], p.R));
+            hi[i] = max(lo[i], min(p.offsets[e + 1], p.R));
         }
-        if (e < G4_MAXE) {
-            s.lo[e] = lo;
-            s.hi[e] = hi;
-        }
-        n[i] = (hi - lo + p.cols - 1) / p.cols;
-        sum += n[i];
+        n[i] = (hi[i] - lo[i] + p.cols - 1) / p.cols;
+        sum.x += n[i] > 0;
+        sum.y += n[i];
     }
-    const int own = sum;
+    const int2 own = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
+        const int x = __shfl_up_sync(0xffffffffu, sum.x, o), y = __shfl_up_sync(0xffffffffu, sum.y, o);
+        if (lane >= o) {
+            sum.x += x;
+            sum.y += y;
+        }
     }
     if (lane == 31) s.wsum[warp] = sum;
     __syncthreads();
-    int before = 0;
+    int2 at = {sum.x - own.x, sum.y - own.y}, all = {0, 0};
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) before += w < warp ? s.wsum[w] : 0;
-    int at = before + sum - own;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        if (PER * tid + i < G4_MAXE) s.blk[PER * tid + i] = at;
-        at += n[i];
+    for (int w = 0; w < WARPS; ++w) {
+        const int2 v = s.wsum[w];
+        if (w < warp) {
+            at.x += v.x;
+            at.y += v.y;
+        }
+        all.x += v.x;
+        all.y += v.y;
     }
-    if (tid == 32 * WARPS - 1) s.blk[G4_MAXE] = before + sum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (n[i] > 0) {
+            s.blk[at.x] = at.y;
+            s.e[at.x] = PER * tid + i;
+            s.lo[at.x] = lo[i];
+            s.hi[at.x] = hi[i];
+            ++at.x;
+            at.y += n[i];
+        }
+    if (tid == 0) {
+        s.blk[all.x] = all.y;
+        s.count = all.x;
+    }
     __syncthreads();
-    return s.blk[G4_MAXE];
+    return all.y;
 }
 
 // A value that is the same in all lanes, told to the compiler (it then lives in a
@@ -271,23 +288,22 @@ __device__ __forceinline__ int g4_rows(G4Rows& s, const G4Params& p) {
 __device__ __forceinline__ int g4_uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // A unit: row-groups of a matrix against the columns of a slot (one pass over the
-// matrix of expert e).
+// matrix of the i-th expert with rows).
 struct G4Walk {
-    int slot, unit, e;
-    // by all lanes of a warp, or (ONE) by one thread
-    template <bool ONE = false>
+    int slot, unit, i;
     __device__ __forceinline__ void start(int u, const G4Rows* s, const G4Params& p) {
         slot = u / p.units;
         unit = u % p.units;
-        e = 0;
-        if (p.offsets) {    // the largest e with blk[e] <= slot
-            for (int hi = p.E; hi - e > 1;) {
-                const int mid = (e + hi) >> 1;
-                if (s->blk[mid] <= slot) e = mid;
-                else hi = mid;
-            }
-            if constexpr (!ONE) e = g4_uniform(e);
+        i = p.offsets ? find(slot, s) : 0;
+    }
+    static __device__ __forceinline__ int find(int slot, const G4Rows* s) {   // the largest i with blk[i] <= slot
+        int i = 0;
+        for (int hi = s->count; hi - i > 1;) {
+            const int mid = (i + hi) >> 1;
+            if (s->blk[mid] <= slot) i = mid;
+            else hi = mid;
         }
+        return i;
     }
     __device__ __forceinline__ void step(int by, const G4Rows* s, const G4Params& p) {
         unit += by;
@@ -297,22 +313,25 @@ struct G4Walk {
             ++slot;
         } while (unit >= p.units);
         if (p.offsets) {
-            while (e + 1 < p.E && s->blk[e + 1] <= slot) ++e;
-            e = g4_uniform(e);
+            while (i + 1 < s->count && s->blk[i + 1] <= slot) ++i;
+            i = g4_uniform(i);
         }
     }
+    __device__ __forceinline__ long long expert(const G4Rows* s, const G4Params& p) const {
+        return p.offsets ? g4_uniform(s->e[i]) : 0;
+    }
     __device__ __forceinline__ int row(const G4Rows* s, const G4Params& p) const {
-        return p.offsets ? s->lo[e] + p.cols * (slot - s->blk[e]) : 0;
+        return p.offsets ? s->lo[i] + p.cols * (slot - s->blk[i]) : 0;
     }
     __device__ __forceinline__ int cols(const G4Rows* s, const G4Params& p, int row) const {
-        return min(p.cols, (p.offsets ? s->hi[e] : p.R) - row);
+        return min(p.cols, (p.offsets ? s->hi[i] : p.R) - row);
     }
 };
 
 // The x that is in shared memory: the columns of slots first .. end - 1.
 constexpr int G4_COLS = 32;
 struct G4Phase {
-    int first, end, cols, products;
+    int end, cols, products;
     int row[G4_COLS];                // of a column: its row of x, the place of its (first) sum
     int sum[G4_COLS];
     uint32_t top[G4_COLS];           // largest |x|, as fp32 bits
@@ -320,94 +339,109 @@ struct G4Phase {
     int slot_col[G4_COLS], slot_prod[G4_COLS];   // of a slot: its first column and product
 };
 
-// As many slots from f on as there is room for, up to the one of the CTA's last
-// unit.  One thread.
+// As many slots from `first` on as there is room for, up to `last`: one warp, a lane per
+// slot.
 template <int XT, int G>
-__device__ void g4_plan(G4Phase& ph, G4Walk f, int last_slot, const G4Rows* s, const G4Params& p) {
+__device__ __forceinline__ void g4_plan(G4Phase& ph, int first, int last, const G4Rows* s, const G4Params& p) {
     constexpr int P = G4X<XT>::PARTS, CO = G4X<XT>::COLS;
-    ph.first = f.slot;
-    int cols = 0, products = 0, n = 0;
-    for (;;) {
-        const int row = f.row(s, p), c = f.cols(s, p, row), q = (c + CO - 1) / CO;
-        if (n && (cols + c > G4_COLS ||
-                  (p.c1 - p.c0) * g4_x_bytes(G, products + q + 1, (cols + c) * P) > p.x_room))
-            break;
-        ph.slot_col[n] = cols;
-        ph.slot_prod[n] = products;
-        for (int j = 0; j < c; ++j) {
-            ph.row[cols + j] = row + j;
-            ph.sum[cols + j] = (products + j / CO) * 8 + j % CO * (8 / CO);
-            ph.top[cols + j] = 0;
-        }
-        cols += c;
-        products += q;
-        ++n;
-        if (f.slot == last_slot || cols == G4_COLS) break;
-        ++f.slot;
-        while (f.e + 1 < p.E && s->blk[f.e + 1] <= f.slot) ++f.e;
+    const int lane = threadIdx.x & 31;
+    G4Walk f = {first + lane, 0, 0};
+    int row = 0, c = 0;
+    if (f.slot <= last) {
+        if (p.offsets) f.i = G4Walk::find(f.slot, s);
+        row = f.row(s, p);
+        c = f.cols(s, p, row);
     }
-    ph.end = ph.first + n;
-    ph.cols = cols;
-    ph.products = products + 1;      // a second product may be read where a slot has only one
+    const int q = (c + CO - 1) / CO;
+    int cols = c, products = q;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, cols, o), y = __shfl_up_sync(0xffffffffu, products, o);
+        if (lane >= o) {
+            cols += x;
+            products += y;
+        }
+    }
+    // a second product may be read where a slot has only one
+    const bool fits = f.slot <= last && (lane == 0 || (cols <= G4_COLS && (p.c1 - p.c0) * g4_x_bytes(G, products + 1, cols * P) <= p.x_room));
+    const unsigned no = ~__ballot_sync(0xffffffffu, fits);
+    const int n = no ? __ffs(no) - 1 : 32;
+    if (lane < n) {
+        ph.slot_col[lane] = cols - c;
+        ph.slot_prod[lane] = products - q;
+        for (int j = 0; j < c; ++j) {
+            ph.row[cols - c + j] = row + j;
+            ph.sum[cols - c + j] = (products - q + j / CO) * 8 + j % CO * (8 / CO);
+            ph.top[cols - c + j] = 0;
+        }
+    }
+    if (lane == n - 1) {
+        ph.end = first + n;
+        ph.cols = cols;
+        ph.products = products + 1;
+    }
 }
 
-// x of the planned columns into shared memory, by all warps.
-template <int XT, int G, bool Z>
+// x of the planned columns into shared memory, by all warps.  The loops are kept
+// rolled here and in the kernel's start: this code runs once per launch, from a cold
+// instruction cache, and its size is its cost.
+template <int XT, int G, bool Z, int WARPS>
 __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, uint8_t* xs) {
-    constexpr int P = G4X<XT>::PARTS, XB = G4X<XT>::BYTES, WARPS = G4X<XT>::WARPS;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int chunks = p.c1 - p.c0, tile = ph.cols * P * 64, items = ph.cols * chunks;
-    const int x_chunk = g4_x_bytes(G, ph.products, ph.cols * P);
-    auto load = [&](int col, int c, float v[4]) {
-        const int k = (p.c0 + c) * G4_CHUNK + 4 * lane;
-        v[0] = v[1] = v[2] = v[3] = 0.f;
-        if (k < p.K) g4_load_x<XT>((const uint8_t*)p.x + ((long long)ph.row[col] * p.K + k) * XB, v);
-    };
-    for (int i = warp; i < items; i += WARPS) {
-        const int col = i / chunks;
-        float v[4];
-        load(col, i - col * chunks, v);
-        uint32_t m = 0;
+    constexpr int P = G4X<XT>::PARTS, XB = G4X<XT>::BYTES;
+    const int lane = threadIdx.x & 31, warp = g4_uniform(threadIdx.x >> 5);
+    const int chunks = p.c1 - p.c0, cols = g4_uniform(ph.cols), products = g4_uniform(ph.products);
+    const int tile = cols * P * 64, x_chunk = g4_x_bytes(G, products, cols * P);
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        int col = 0, c = warp;
+        while (true) {
+            while (c >= chunks) {
+                c -= chunks;
+                ++col;
+            }
+            if (col >= cols) break;
+            const int k = (p.c0 + c) * G4_CHUNK + 4 * lane;
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            if (k < p.K) g4_load_x<XT>((const uint8_t*)p.x + ((long long)ph.row[col] * p.K + k) * XB, v);
+            if (pass == 0) {
+                uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0 && m) atomicMax(&ph.top[col], m);
-    }
-    __syncthreads();
-    for (int i = warp; i < items; i += WARPS) {
-        const int col = i / chunks, c = i - col * chunks;
-        float v[4];
-        load(col, c, v);
-        const uint32_t top = ph.top[col];
-        // the largest lands in [2^13, 2^14); at most 2^126, which still keeps the smallest columns whole
-        const int E = min(126, 13 + 127 - (int)(top >> 23));
-        const float up = __uint_as_float((uint32_t)(127 + E) << 23);
-        if (c == 0 && lane == 0)
-            ph.down[col] = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : (uint32_t)(127 - E) << 23);
-        // k = 32 (lane / 8) + 4 (lane % 8): columns 8t + 0, 1 (times 1) and 8t + 2, 3 (by 16), or + 4, 5 and + 6, 7
-        v[0] *= up; v[1] *= up;
-        v[2] *= up * 0.0625f; v[3] *= up * 0.0625f;
-        uint8_t* at = xs + c * x_chunk;
-        uint8_t* bytes = at + (lane >> 3) * tile + col * (P * 64) + (lane & 7) * 8;
+                for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+                m = __reduce_max_sync(0xffffffffu, m);
+                if (lane == 0 && m) atomicMax(&ph.top[col], m);
+            } else {
+                const uint32_t top = ph.top[col];
+                // the largest lands in [2^13, 2^14); at most 2^126, which still keeps the smallest columns whole
+                const int E = min(126, 13 + 127 - (int)(top >> 23));
+                const float up = __uint_as_float((uint32_t)(127 + E) << 23);
+                if (c == 0 && lane == 0)
+                    ph.down[col] = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : (uint32_t)(127 - E) << 23);
+                // k = 32 (lane / 8) + 4 (lane % 8): columns 8t + 0, 1 (times 1) and 8t + 2, 3 (by 16), or + 4, 5 and + 6, 7
+                v[0] *= up; v[1] *= up;
+                v[2] *= up * 0.0625f; v[3] *= up * 0.0625f;
+                uint8_t* at = xs + c * x_chunk;
+                uint8_t* bytes = at + (lane >> 3) * tile + col * (P * 64) + (lane & 7) * 8;
+                float* sums = reinterpret_cast<float*>(at + 4 * tile) + lane / (G / 4) * products * 8 + ph.sum[col];
+#pragma unroll 1
+                for (int q = 0; q < P; ++q) {
+                    const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+                    uint2 o;
+                    memcpy(&o.x, &a, 4);
+                    memcpy(&o.y, &b, 4);
+                    *reinterpret_cast<uint2*>(bytes + q * 64) = o;
+                    const float2 f = __half22float2(a), h = __half22float2(b);
+                    v[0] = (v[0] - f.x) * 2048.f; v[1] = (v[1] - f.y) * 2048.f;
+                    v[2] = (v[2] - h.x) * 2048.f; v[3] = (v[3] - h.y) * 2048.f;
+                    float s = fmaf(h.x + h.y, 16.f, f.x + f.y);
 #pragma unroll
-        for (int q = 0; q < P; ++q) {
-            const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
-            uint2 o;
-            memcpy(&o.x, &a, 4);
-            memcpy(&o.y, &b, 4);
-            *reinterpret_cast<uint2*>(bytes + q * 64) = o;
-            const float2 f = __half22float2(a), h = __half22float2(b);
-            v[0] = (v[0] - f.x) * 2048.f; v[1] = (v[1] - f.y) * 2048.f;
-            v[2] = (v[2] - h.x) * 2048.f; v[3] = (v[3] - h.y) * 2048.f;
-            float s = fmaf(h.x + h.y, 16.f, f.x + f.y);
-#pragma unroll
-            for (int d = 1; d < G / 4; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            if (lane % (G / 4) == 0)
-                reinterpret_cast<float*>(at + 4 * tile)[lane / (G / 4) * ph.products * 8 + ph.sum[col] + q] =
-                    s * (Z ? -0x1.0p-21f : -0x1.0p-18f);
+                    for (int d = 1; d < G / 4; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+                    if (lane % (G / 4) == 0) sums[q] = s * (Z ? -0x1.0p-21f : -0x1.0p-18f);
+                }
+            }
+            c += WARPS;
         }
+        __syncthreads();
     }
-    __syncthreads();
 }
 
 // A unit is two row-groups against up to p.cols rows of x: rows 32u .. 32u + 31
@@ -420,10 +454,10 @@ __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, uint8
 // and are added in warp order.  That is put off until the team's buffer is full (8 units
 // of one column, 1 of 8), so that the warps of a team wait for one another as rarely
 // as they can.
-template <int XT, int G, bool Z, bool PAIR>
-__global__ void __launch_bounds__(G4X<XT>::WARPS * 32, 1) g4_kernel(G4Params p) {
+template <int XT, int G, bool Z, bool PAIR, int NBMAX>
+__global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p) {
     constexpr int FULL = g4_chunk_bytes(G4_CHUNK, G, Z);
-    constexpr int P = G4X<XT>::PARTS, WARPS = G4X<XT>::WARPS;
+    constexpr int P = G4X<XT>::PARTS, WARPS = g4_warps(NBMAX);
     constexpr int STAGE = G4_NR * FULL, RING = 2 * STAGE;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int2 wait_all[WARPS][8];   // (unit, row of y) of the blocks of 32 sums that wait
@@ -460,7 +494,7 @@ __global__ void __launch_bounds__(G4X<XT>::WARPS * 32, 1) g4_kernel(G4Params p) 
     const uint8_t *f0 = nullptr, *f1 = nullptr, *f2 = nullptr;         // the lane's pieces: codes of both, and behind
     G4Walk f = w;
     auto aim = [&]() {
-        const long long at = f.e * p.stride + (long long)(p.c0 + member) * FULL;
+        const long long at = f.expert(rows, p) * p.stride + (long long)(p.c0 + member) * FULL;
         const uint8_t *r0, *r1;
         if constexpr (PAIR) {
             r0 = p.W0 + at + f.unit * p.rg_bytes;
@@ -502,8 +536,8 @@ __global__ void __launch_bounds__(G4X<XT>::WARPS * 32, 1) g4_kernel(G4Params p) 
         fstage ^= STAGE;
     };
     if (fl) aim();
-    fetch();
-    fetch();
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) fetch();
 
     const int g = lane >> 2, t = lane & 3;
     int used = 0, stage = 0;   // used: blocks of 32 sums in the buffer
@@ -578,34 +612,38 @@ __global__ void __launch_bounds__(G4X<XT>::WARPS * 32, 1) g4_kernel(G4Params p) 
                     }
             }
     };
-    for (int u = u0 + team;; ) {
+    for (int u = u0 + team;;) {
         // x of the next slots, when the CTA is through with the last ones
-        if (threadIdx.x == 0) {
-            G4Walk q = w;
-            q.start<true>(phase_end < 0 ? u0 : phase_end * p.units, rows, p);
-            g4_plan<XT, G>(ph, q, (u1 - 1) / p.units, rows, p);
-        }
+        first = phase_end < 0 ? u0 / p.units : phase_end;
+        if (warp == 0) g4_plan<XT, G>(ph, first, (u1 - 1) / p.units, rows, p);
         __syncthreads();
-        first = ph.first;
         phase_end = g4_uniform(ph.end);
         products = g4_uniform(ph.products);
         tile = g4_uniform(ph.cols) * P * 64;
         x_chunk = g4_x_bytes(G, products, g4_uniform(ph.cols) * P);
-        g4_stage_x<XT, G, Z>(p, ph, xs);
-        for (; u < u1 && w.slot < phase_end; u += teams) {
-            const int row0 = g4_uniform(w.row(rows, p)), cols = g4_uniform(w.cols(rows, p, row0));
+        g4_stage_x<XT, G, Z, WARPS>(p, ph, xs);
+        const bool done = phase_end * (long long)p.units >= u1;   // the CTA's last slots
+#pragma unroll 1
+        while (true) {
+            const bool more = u < u1 && w.slot < phase_end;
+            int row0 = 0, cols = 0;
+            if (more) {
+                row0 = g4_uniform(w.row(rows, p));
+                cols = g4_uniform(w.cols(rows, p, row0));
+            }
+            if (more ? used + cols > 8 : done && used) flush();
+            if (!more) break;
             const int col0 = g4_uniform(ph.slot_col[w.slot - first]), prod0 = g4_uniform(ph.slot_prod[w.slot - first]);
-            if (used + cols > 8) flush();
-            if (P == 1 || cols <= 2) unit(std::integral_constant<int, 1>(), cols, col0, prod0);
-            else unit(std::integral_constant<int, P == 1 ? 1 : 2>(), cols, col0, prod0);
+            if (NBMAX == 1 || cols <= 2) unit(std::integral_constant<int, 1>(), cols, col0, prod0);
+            else unit(std::integral_constant<int, NBMAX>(), cols, col0, prod0);
             if (member == 0 && lane < cols) wait_all[team][used + lane] = make_int2(w.unit, row0 + lane);
             used += cols;
+            u += teams;
             w.step(teams, rows, p);
         }
-        if (phase_end * (long long)p.units >= u1) break;
+        if (done) break;
         __syncthreads();   // x is written again
     }
-    if (used) flush();
 }
 
 // Warps per unit: the least time of the busiest team, a unit costing its chunks and
@@ -625,22 +663,21 @@ inline int g4_team(long long units, int chunks, int sms, int warps) {
     return best;
 }
 
-template <int XT, int G, bool Z, bool PAIR>
-cudaError_t g4_launch_p(G4Params p, cudaStream_t stream) {
+template <int XT, int G, bool Z, bool PAIR, int NBMAX>
+cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
     int sms = 0;
     cudaError_t e = device_sms(sms);
     if (e != cudaSuccess) return e;
-    constexpr int P = G4X<XT>::PARTS, CO = G4X<XT>::COLS, WARPS = G4X<XT>::WARPS;
+    constexpr int P = G4X<XT>::PARTS, CO = G4X<XT>::COLS, WARPS = g4_warps(NBMAX);
     constexpr int FULL = g4_chunk_bytes(G4_CHUNK, G, Z);
     const int fixed = WARPS * 1024 + WARPS * 2 * G4_NR * FULL + (p.offsets ? (int)sizeof(G4Rows) : 0);
     const int room = (G4_SMEM - (int)sizeof(G4Phase) - WARPS * 64 - 512 - fixed) & ~127;   // less the kernel's static part
     p.rg_bytes = g4_rowgroup_bytes(p.K, G, Z);
     p.units = PAIR ? (p.N + 15) / 16 : (p.N + 31) / 32;
     const int chunks = (p.K + G4_CHUNK - 1) / G4_CHUNK;
-    // columns of a pass: as many as there can be, up to 8 (fp32 x: 4, two products), with the x of all of K
-    // in shared memory.  Where that does not fit, fewer columns a pass (gate/up, whose sums have to be
+    // columns of a pass: as many as there can be, with the x of all of K in shared memory.  Where that does not fit, fewer columns a pass (gate/up, whose sums have to be
     // whole before silu) or K in parts, one launch each (the weights are then still read once).
-    p.cols = std::min(p.R, P == 1 ? 8 : 4);
+    p.cols = std::min(p.R, NBMAX * CO);
     int span = 0, x_chunk = 0;
     while (true) {
         x_chunk = g4_x_bytes(G, (p.cols + CO - 1) / CO + 1, p.cols * P);
@@ -655,7 +692,7 @@ cudaError_t g4_launch_p(G4Params p, cudaStream_t stream) {
     const long long total = (long long)p.units * (p.offsets ? p.R : 1);
     const int grid = (int)std::min<long long>(sms, total);
     const int smem = fixed + p.x_room;
-    auto kernel = g4_kernel<XT, G, Z, PAIR>;
+    auto kernel = g4_kernel<XT, G, Z, PAIR, NBMAX>;
     static SmemLimit limit;   // one per instantiation
     e = limit.ensure((const void*)kernel, smem);
     const int all = p.R;
@@ -671,6 +708,14 @@ cudaError_t g4_launch_p(G4Params p, cudaStream_t stream) {
         }
     }
     return e;
+}
+
+template <int XT, int G, bool Z, bool PAIR>
+cudaError_t g4_launch_p(const G4Params& p, cudaStream_t stream) {
+    // fp32 x: two products a pass (4 columns) where there are that many columns to an expert
+    if constexpr (XT == 1)
+        if (p.R > 2 * (p.offsets ? p.E : 1)) return g4_launch_n<XT, G, Z, PAIR, 2>(p, stream);
+    return g4_launch_n<XT, G, Z, PAIR, 1>(p, stream);
 }
 
 template <int XT, int G>
