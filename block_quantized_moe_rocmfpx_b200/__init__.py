@@ -207,50 +207,84 @@ def moe_router_project_topk(w_router, bias, x, k: int, logits, idx, w, stream=No
                              _stream(stream)))
 
 
-def _dtype_codes():
-    import torch
-    return {torch.bfloat16: RFX_BF16, torch.float32: RFX_F32, torch.float16: RFX_F16}
+_RT = None   # torch and what the row and 4-bit calls need of it at every call, looked up once
 
 
-_DTYPES = None
+class _Runtime:
+    def __init__(self):
+        import torch
+        self.i32, self.f32, self.u8, self.f16 = torch.int32, torch.float32, torch.uint8, torch.float16
+        self.codes = {torch.bfloat16: RFX_BF16, torch.float32: RFX_F32, torch.float16: RFX_F16}
+        self.device = torch.cuda.current_device
+        # the stream's handle without making a Stream object, where torch offers it
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw if raw is not None else (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _rows_dtype(t) -> int:
-    """rfx_dtype of a tensor's elements."""
-    global _DTYPES
-    if _DTYPES is None:
-        _DTYPES = _dtype_codes()
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"dtype {t.dtype}: bfloat16, float16 or float32 expected")
-    return code
+def _runtime() -> _Runtime:
+    global _RT
+    if _RT is None:
+        _RT = _Runtime()
+    return _RT
 
 
-def _dense(name: str, t, shape, dtype=None):
-    """Check a tensor of a row or 4-bit call: on the current CUDA device, contiguous,
-    of this shape and type (the C call sees only its pointer)."""
-    import torch
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+def _on(name: str, t) -> int:
+    """The device of a call: that of its tensor `t`, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0 or dev != _runtime().device():
+        raise ValueError(f"{name}: must be on the current CUDA device, not {t.device}")
+    return dev
+
+
+def _dense(name: str, t, dev: int, shape, dtype=None):
+    """Check a tensor of a row or 4-bit call: on device dev, contiguous, of this
+    shape and type (the C call sees only its pointer)."""
+    if t.get_device() == dev and t.shape == shape and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return
+    if t.get_device() != dev:
         raise ValueError(f"{name}: must be on the current CUDA device, not {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _bytes_at_least(name: str, t, dev: int, n: int):
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: must be on the current CUDA device, not {t.device}")
+    if t.numel() * t.element_size() < n:
+        raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, at least {n} expected")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
+
+
+def _type_code(name: str, t) -> int:
+    """rfx_dtype of a tensor's elements."""
+    code = _RT.codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected bfloat16, float16 or float32")
+    return code
+
+
+def _on_stream(stream, dev: int) -> int:
+    return _RT.stream(dev) if stream is None else _stream(stream)
 
 
 def moe_router_topk_backward(idx, w, dw, dlogits, stream=None):
     """dlogits fp32 [T][E] from dw fp32 [T][k], the gradient of moe_router_topk's w
     (idx int32 / w fp32 [T][k] as it wrote them)."""
-    import torch
+    dev = _on("dlogits", dlogits)
     T, E = dlogits.shape
     k = idx.shape[-1]
-    _dense("dlogits", dlogits, (T, E), torch.float32)
-    _dense("idx", idx, (T, k), torch.int32)
-    _dense("w", w, (T, k), torch.float32)
-    _dense("dw", dw, (T, k), torch.float32)
-    _check(_router_bwd(_ptr(idx), _ptr(w), _ptr(dw), T, E, k, _ptr(dlogits), _stream(stream)))
+    rt, tk = _RT, (T, k)
+    _dense("dlogits", dlogits, dev, (T, E), rt.f32)
+    _dense("idx", idx, dev, tk, rt.i32)
+    _dense("w", w, dev, tk, rt.f32)
+    _dense("dw", dw, dev, tk, rt.f32)
+    rc = _router_bwd(idx.data_ptr(), w.data_ptr(), dw.data_ptr(), T, E, k, dlogits.data_ptr(), _on_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def moe_group_workspace_bytes(T: int, k: int, E: int) -> int:
@@ -261,64 +295,78 @@ def moe_group_tokens(x, idx, E: int, xs, pos, rows, offsets, ws, stream=None):
     """Rows of x [T][H] sorted by expert: xs [T*k][H], pos int32 [T][k], rows int32
     [T*k], offsets int32 [E+1] from idx int32 [T][k] (device tensors; x and xs may
     both be None).  ws: moe_group_workspace_bytes(T, k, E) bytes, rfx_ws_init once."""
-    import torch
+    dev = _on("idx", idx)
     T, k = idx.shape
-    _dense("idx", idx, (T, k), torch.int32)
-    _dense("pos", pos, (T, k), torch.int32)
-    _dense("rows", rows, (T * k,), torch.int32)
-    _dense("offsets", offsets, (E + 1,), torch.int32)
+    i32 = _RT.i32
+    _dense("idx", idx, dev, (T, k), i32)
+    _dense("pos", pos, dev, (T, k), i32)
+    _dense("rows", rows, dev, (T * k,), i32)
+    _dense("offsets", offsets, dev, (E + 1,), i32)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws: must be contiguous and on the current CUDA device")
     if (x is None) != (xs is None):
         raise ValueError("x and xs: both or neither")
-    H, dt = 1, RFX_F32
+    H, dt, px, pxs = 1, RFX_F32, None, None
     if x is not None:
-        H, dt = x.shape[-1], _rows_dtype(x)
-        _dense("x", x, (T, H))
-        _dense("xs", xs, (T * k, H), x.dtype)
-    _check(_group(_ptr(x), dt, T, H, _ptr(idx), k, E, _ptr(xs), _ptr(pos), _ptr(rows), _ptr(offsets), _ptr(ws),
-                  ws.numel() * ws.element_size(), _stream(stream)))
+        H, dt = x.shape[-1], _type_code("x", x)
+        _dense("x", x, dev, (T, H))
+        _dense("xs", xs, dev, (T * k, H), x.dtype)
+        px, pxs = x.data_ptr(), xs.data_ptr()
+    rc = _group(px, dt, T, H, idx.data_ptr(), k, E, pxs, pos.data_ptr(), rows.data_ptr(), offsets.data_ptr(),
+                ws.data_ptr(), ws.numel() * ws.element_size(), _on_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def moe_group_tokens_backward(dxs, pos, dx, stream=None):
     """dx [T][H] = sum over j of dxs[pos[t][j]] (dxs [T*k][H] of dx's type, pos int32 [T][k])."""
-    import torch
+    dev = _on("pos", pos)
     T, k = pos.shape
     H = dx.shape[-1]
-    _dense("pos", pos, (T, k), torch.int32)
-    _dense("dxs", dxs, (T * k, H), dx.dtype)
-    _dense("dx", dx, (T, H))
-    _check(_group_bwd(_ptr(dxs), _rows_dtype(dx), T, H, _ptr(pos), k, _ptr(dx), _stream(stream)))
+    _dense("pos", pos, dev, (T, k), _RT.i32)
+    _dense("dxs", dxs, dev, (T * k, H), dx.dtype)
+    _dense("dx", dx, dev, (T, H))
+    rc = _group_bwd(dxs.data_ptr(), _type_code("dx", dx), T, H, pos.data_ptr(), k, dx.data_ptr(),
+                    _on_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def moe_combine_rows(ys, pos, w, y, base=None, stream=None):
     """y [T][H] = base + sum over j of w[t][j] * ys[pos[t][j]] (ys [T*k][H], pos int32
     and w fp32 [T][k]; y and base of ys's type or fp32)."""
-    import torch
+    dev = _on("pos", pos)
     T, k = pos.shape
     H = y.shape[-1]
-    _dense("pos", pos, (T, k), torch.int32)
-    _dense("w", w, (T, k), torch.float32)
-    _dense("ys", ys, (T * k, H))
-    _dense("y", y, (T, H))
+    _dense("pos", pos, dev, (T, k), _RT.i32)
+    _dense("w", w, dev, (T, k), _RT.f32)
+    _dense("ys", ys, dev, (T * k, H))
+    _dense("y", y, dev, (T, H))
     if base is not None:
-        _dense("base", base, (T, H), y.dtype)
-    _check(_combine(_ptr(ys), _rows_dtype(ys), T, H, _ptr(pos), k, _ptr(w), _ptr(base), _ptr(y), _rows_dtype(y),
-                    _stream(stream)))
+        _dense("base", base, dev, (T, H), y.dtype)
+        base = base.data_ptr()
+    rc = _combine(ys.data_ptr(), _type_code("ys", ys), T, H, pos.data_ptr(), k, w.data_ptr(), base, y.data_ptr(),
+                  _type_code("y", y), _on_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def moe_combine_rows_backward(dy, ys, pos, w, dys, dw, stream=None):
     """dys [T*k][H] and dw fp32 [T][k], the gradients of moe_combine_rows from dy [T][H]
     (of ys's type or fp32)."""
-    import torch
+    dev = _on("pos", pos)
     T, k = pos.shape
     H = dy.shape[-1]
-    _dense("pos", pos, (T, k), torch.int32)
-    _dense("w", w, (T, k), torch.float32)
-    _dense("ys", ys, (T * k, H))
-    _dense("dys", dys, (T * k, H), ys.dtype)
-    _dense("dy", dy, (T, H))
-    _dense("dw", dw, (T, k), torch.float32)
-    _check(_combine_bwd(_ptr(dy), _rows_dtype(dy), _ptr(ys), _rows_dtype(ys), T, H, _ptr(pos), k, _ptr(w), _ptr(dys),
-                        _ptr(dw), _stream(stream)))
+    _dense("pos", pos, dev, (T, k), _RT.i32)
+    _dense("w", w, dev, (T, k), _RT.f32)
+    _dense("ys", ys, dev, (T * k, H))
+    _dense("dys", dys, dev, (T * k, H), ys.dtype)
+    _dense("dy", dy, dev, (T, H))
+    _dense("dw", dw, dev, (T, k), _RT.f32)
+    rc = _combine_bwd(dy.data_ptr(), _type_code("dy", dy), ys.data_ptr(), _type_code("ys", ys), T, H, pos.data_ptr(), k,
+                      w.data_ptr(), dys.data_ptr(), dw.data_ptr(), _on_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def rfx_gemv_q(fmt: int, W, N: int, K: int, x, y, stream=None):
@@ -366,65 +414,66 @@ def rfx_g4_unpack(packed: np.ndarray, rows: int, cols: int, group: int, zeros: b
     return codes, scales, z
 
 
-def _bytes_at_least(name: str, t, n: int):
-    import torch
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name}: must be on the current CUDA device, not {t.device}")
-    if t.numel() * t.element_size() < n:
-        raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, at least {n} expected")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-
-
 def rfx_g4_pack_device(codes, scales, zeros, rows: int, cols: int, group: int, dst, stream=None):
     """Pack device tensors (codes uint8 [rows][cols], scales float16 and zeros uint8 or
     None [rows][cols/group]) into device dst (rfx_g4_packed_bytes bytes)."""
-    import torch
-    _dense("codes", codes, (rows, cols), torch.uint8)
-    _dense("scales", scales, (rows, cols // max(group, 1)), torch.float16)
+    dev = _on("codes", codes)
+    per = (rows, cols // max(group, 1))
+    _dense("codes", codes, dev, (rows, cols), _RT.u8)
+    _dense("scales", scales, dev, per, _RT.f16)
     if zeros is not None:
-        _dense("zeros", zeros, (rows, cols // max(group, 1)), torch.uint8)
-    _bytes_at_least("dst", dst, rfx_g4_packed_bytes(rows, cols, group, zeros is not None))
-    _check(_g4_pack_device(_ptr(codes), _ptr(scales), _ptr(zeros), rows, cols, group, _ptr(dst), _stream(stream)))
+        _dense("zeros", zeros, dev, per, _RT.u8)
+    _bytes_at_least("dst", dst, dev, rfx_g4_packed_bytes(rows, cols, group, zeros is not None))
+    _check(_g4_pack_device(_ptr(codes), _ptr(scales), _ptr(zeros), rows, cols, group, _ptr(dst),
+                           _on_stream(stream, dev)))
 
 
 def rfx_gemv_g4(W, N: int, K: int, group: int, x, y, zeros: bool = False, stream=None):
     """y fp32 [q][N] = W x for packed G4 weights W [N][K] and x [q][K] (bf16, fp16 or
     fp32, q <= 8; device tensors).  zeros: W was packed with zero points."""
-    import torch
-    q = x.shape[0]
-    _dense("x", x, (q, K))
-    _dense("y", y, (q, N), torch.float32)
-    _bytes_at_least("W", W, rfx_g4_packed_bytes(N, K, group, zeros))
-    _check(_gemv_g4(_ptr(W), N, K, group, 1 if zeros else 0, _ptr(x), _rows_dtype(x), q, _ptr(y), _stream(stream)))
+    dev = _on("x", x)
+    q, z = x.shape[0], 1 if zeros else 0
+    _dense("x", x, dev, (q, K))
+    _dense("y", y, dev, (q, N), _RT.f32)
+    _bytes_at_least("W", W, dev, _g4_bytes(N, K, group, z))
+    rc = _gemv_g4(W.data_ptr(), N, K, group, z, x.data_ptr(), _type_code("x", x), q, y.data_ptr(),
+                  _on_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def _experts_g4(x, offsets, y, N, K):
-    import torch
+    dev = _on("x", x)
     R, E = x.shape[0], offsets.shape[0] - 1
-    _dense("x", x, (R, K))
-    _dense("offsets", offsets, (E + 1,), torch.int32)
-    _dense("y", y, (R, N), torch.float32)
-    return R, E
+    _dense("x", x, dev, (R, K))
+    _dense("offsets", offsets, dev, (E + 1,), _RT.i32)
+    _dense("y", y, dev, (R, N), _RT.f32)
+    return dev, R, E
 
 
 def moe_gemv_g4(W, stride: int, N: int, K: int, group: int, x, offsets, y, zeros: bool = False, stream=None):
     """y[r] = W_e x[r] for the rows r of expert e (offsets int32 [E+1]): x [R][K] bf16,
     fp16 or fp32, y fp32 [R][N], W: E packed G4 matrices `stride` bytes apart."""
-    R, E = _experts_g4(x, offsets, y, N, K)
-    _bytes_at_least("W", W, (E - 1) * stride + rfx_g4_packed_bytes(N, K, group, zeros))
-    _check(_moe_g4(_ptr(W), stride, E, N, K, group, 1 if zeros else 0, _ptr(x), _rows_dtype(x), _ptr(offsets), R,
-                   _ptr(y), _stream(stream)))
+    dev, R, E = _experts_g4(x, offsets, y, N, K)
+    z = 1 if zeros else 0
+    _bytes_at_least("W", W, dev, (E - 1) * stride + _g4_bytes(N, K, group, z))
+    rc = _moe_g4(W.data_ptr(), stride, E, N, K, group, z, x.data_ptr(), _type_code("x", x), offsets.data_ptr(), R,
+                 y.data_ptr(), _on_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def moe_gate_up_g4(gate, up, stride: int, N: int, K: int, group: int, x, offsets, h, zeros: bool = False, stream=None):
     """h[r] = silu(gate_e x[r]) * (up_e x[r]) for the rows r of expert e; arguments as moe_gemv_g4."""
-    R, E = _experts_g4(x, offsets, h, N, K)
-    n = (E - 1) * stride + rfx_g4_packed_bytes(N, K, group, zeros)
-    _bytes_at_least("gate", gate, n)
-    _bytes_at_least("up", up, n)
-    _check(_moe_gate_up_g4(_ptr(gate), _ptr(up), stride, E, N, K, group, 1 if zeros else 0, _ptr(x), _rows_dtype(x),
-                           _ptr(offsets), R, _ptr(h), _stream(stream)))
+    dev, R, E = _experts_g4(x, offsets, h, N, K)
+    z = 1 if zeros else 0
+    n = (E - 1) * stride + _g4_bytes(N, K, group, z)
+    _bytes_at_least("gate", gate, dev, n)
+    _bytes_at_least("up", up, dev, n)
+    rc = _moe_gate_up_g4(gate.data_ptr(), up.data_ptr(), stride, E, N, K, group, z, x.data_ptr(), _type_code("x", x),
+                         offsets.data_ptr(), R, h.data_ptr(), _on_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def moe_layer_create(desc: moe_layer_desc) -> int:
