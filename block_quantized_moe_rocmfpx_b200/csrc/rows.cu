@@ -42,15 +42,68 @@ __global__ void __launch_bounds__(GT) group_count_kernel(GroupParams p) {
     for (int e = threadIdx.x; e < group_pitch(p.E); e += GT) out[e] = e < p.E ? hist[e] : 0;
 }
 
+// Copies of a CTA's rows by bulk stores: a warp brings a piece of a token's row into
+// one of its GROUP_SLOTS buffers in shared memory (cp.async), and lanes 0 .. k - 1 each
+// store it whole to one of the rows that it goes to.  Pieces of later tokens are on their
+// way meanwhile; a buffer is filled again once its stores have read it.
+constexpr int GROUP_PIECE = 4096;
+constexpr int GROUP_SLOTS = 3;
+constexpr int GROUP_SMEM = GT / 32 * GROUP_SLOTS * GROUP_PIECE;
+
+__device__ __forceinline__ void group_copy(const GroupParams& p, int ta, int nt, const int32_t* s_pos, uint8_t* ring) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int pieces = (int)((p.row_bytes + GROUP_PIECE - 1) / GROUP_PIECE), items = nt * pieces;
+    uint8_t* mine = ring + warp * (GROUP_SLOTS * GROUP_PIECE);
+    const uint32_t mine_s = smem_u32(mine);
+    auto bytes_of = [&](int q) { return (int)min((long long)GROUP_PIECE, p.row_bytes - (long long)q * GROUP_PIECE); };
+    auto load = [&](int i, int slot) {
+        if (i < items) {
+            const int t = i / pieces, q = i - t * pieces, n = bytes_of(q);
+            const uint8_t* src = p.x + (long long)(ta + t) * p.row_bytes + (long long)q * GROUP_PIECE;
+            for (int o = lane * 16; o < n; o += 512)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine_s + slot * GROUP_PIECE + o), "l"(src + o)
+                             : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    load(warp, 0);
+    load(warp + GT / 32, 1);
+    int slot = 0;
+    for (int i = warp; i < items; i += GT / 32) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // every lane's copies, before the bulk stores read them
+        __syncwarp();
+        const int t = i / pieces, q = i - t * pieces;
+        if (lane < p.k) {
+            const int r = s_pos[t * p.k + lane];
+            if (r >= 0) {
+                uint8_t* dst = p.xs + (long long)r * p.row_bytes + (long long)q * GROUP_PIECE;
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                             "r"(mine_s + slot * GROUP_PIECE), "r"(bytes_of(q))
+                             : "memory");
+            }
+        }
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        // the buffer of the piece after next is the one stored before this: all but the last group have been read
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+        load(i + 2 * (GT / 32), slot >= 1 ? slot - 1 : GROUP_SLOTS - 1);
+        slot = slot + 1 == GROUP_SLOTS ? 0 : slot + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // One CTA per slice: first rows of the slice's experts (ONE: by counting all
 // of idx; else from the counts of the slices), the places of its entries in
 // order, and the copies of its tokens' rows.
-template <bool ONE, typename V>
+template <bool ONE, bool BULK, typename V>
 __global__ void __launch_bounds__(GT) group_place_kernel(GroupParams p) {
+    extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(16) int32_t tot[GROUP_MAXE];
     __shared__ __align__(16) int32_t cur[GROUP_MAXE];
     __shared__ int32_t wsum[GT / 32];
-    __shared__ int32_t s_pos[GROUP_BATCH];
+    __shared__ int32_t s_pos[GROUP_BATCH];   // a batch's expert ids, then its places
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dep_launch();
     for (int e = tid; e < GROUP_MAXE; e += GT) {
@@ -63,6 +116,8 @@ __global__ void __launch_bounds__(GT) group_place_kernel(GroupParams p) {
     const int t0 = blockIdx.x * p.per;
     const int t1 = min(t0 + p.per, p.T);
     const long long first = (long long)t0 * p.k;
+    const int tb = GROUP_BATCH / p.k;   // tokens per batch
+    for (int i = tid; i < min(tb, t1 - t0) * p.k; i += GT) s_pos[i] = p.idx[first + i];
     if constexpr (ONE) {
         for (long long i = tid; i < n; i += GT) {
             const int e = p.idx[i];
@@ -77,7 +132,7 @@ __global__ void __launch_bounds__(GT) group_place_kernel(GroupParams p) {
         const int q = tid % quads, l = tid / quads;
         if (l < lines) {
             int4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-#pragma unroll 8
+#pragma unroll 10
             for (int s = l; s < p.slices; s += lines) {
                 const int4 v = *reinterpret_cast<const int4*>(p.part + (long long)s * pitch + 4 * q);
                 a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
@@ -114,9 +169,12 @@ __global__ void __launch_bounds__(GT) group_place_kernel(GroupParams p) {
         }
     }
     __syncthreads();
-    const int tb = GROUP_BATCH / p.k;   // tokens per batch
     for (int ta = t0; ta < t1; ta += tb) {
         const int nt = min(tb, t1 - ta);
+        if (ta > t0) {
+            for (int i = tid; i < nt * p.k; i += GT) s_pos[i] = p.idx[(long long)ta * p.k + i];
+            __syncthreads();
+        }
         if (warp == 0) {
             // 32 entries a step: lanes of one expert rank themselves by lane
             bool bad = false;
@@ -125,7 +183,7 @@ __global__ void __launch_bounds__(GT) group_place_kernel(GroupParams p) {
                 const long long ent = (long long)ta * p.k + m;
                 int e = -1;
                 if (m < nt * p.k) {
-                    e = p.idx[ent];
+                    e = s_pos[m];
                     if ((unsigned)e >= (unsigned)p.E) {
                         bad |= e != -1;
                         e = -1;
@@ -147,15 +205,30 @@ __global__ void __launch_bounds__(GT) group_place_kernel(GroupParams p) {
             if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.ctrl + MOE_CTRL_ERR, MOE_ERR_EXPERT);
         }
         __syncthreads();
-        if (p.x) {
+        if constexpr (BULK) {
+            group_copy(p, ta, nt, s_pos, ring);
+        } else if (p.x) {
+            // `span` threads a token (a power of two, a warp at least), U vectors of its row in flight each
+            constexpr int U = 4;
             const int nv = (int)(p.row_bytes / (long long)sizeof(V));
-            const long long items = (long long)nt * nv;
-            for (long long i = tid; i < items; i += GT) {
-                const int t = (int)(i / nv), c = (int)(i % nv);
-                const V v = reinterpret_cast<const V*>(p.x + (long long)(ta + t) * p.row_bytes)[c];
-                for (int j = 0; j < p.k; ++j) {
-                    const int at = s_pos[t * p.k + j];
-                    if (at >= 0) reinterpret_cast<V*>(p.xs + (long long)at * p.row_bytes)[c] = v;
+            int span = GT;
+            while (span > 32 && GT / span < nt) span >>= 1;
+            for (int t = tid / span; t < nt; t += GT / span) {
+                const V* src = reinterpret_cast<const V*>(p.x + (long long)(ta + t) * p.row_bytes);
+                const int32_t* at = s_pos + t * p.k;
+                for (int c0 = tid & (span - 1); c0 < nv; c0 += U * span) {
+                    V v[U];
+#pragma unroll
+                    for (int i = 0; i < U; ++i)
+                        if (c0 + i * span < nv) v[i] = __ldg(src + c0 + i * span);
+                    for (int j = 0; j < p.k; ++j) {
+                        const int r = at[j];
+                        if (r < 0) continue;
+                        V* dst = reinterpret_cast<V*>(p.xs + (long long)r * p.row_bytes) + c0;
+#pragma unroll
+                        for (int i = 0; i < U; ++i)
+                            if (c0 + i * span < nv) dst[i * span] = v[i];
+                    }
                 }
             }
         }
@@ -179,82 +252,135 @@ struct alignas(sizeof(E) * N < 16 ? sizeof(E) * N : 16) Vec { E v[N]; };
 
 // -------------------------------------------------------------- combine ---
 
-template <typename TI, typename TO, int N>
-__global__ void __launch_bounds__(256) combine_kernel(const TI* __restrict__ ys, int T, int H,
-                                                      const int32_t* __restrict__ pos, int k,
-                                                      const float* __restrict__ w, const TO* base, TO* y,
-                                                      int blocks_per_row) {
-    grid_dep_launch();
-    grid_dep_wait();
-    const int t = blockIdx.x / blocks_per_row;
-    const int c = ((int)(blockIdx.x % blocks_per_row) * 256 + threadIdx.x) * N;
-    if (c >= H) return;
-    const long long R = (long long)T * k;
-    float acc[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    for (int j = 0; j < k; ++j) {
-        const int at = pos[(long long)t * k + j];
-        if ((unsigned long long)(long long)at >= (unsigned long long)R) continue;
-        const Vec<TI, N> v = *reinterpret_cast<const Vec<TI, N>*>(ys + (long long)at * H + c);
-        if (w) {
-            const float wj = w[(long long)t * k + j];
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(wj, to_f(v.v[i]), acc[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] += to_f(v.v[i]);
-        }
-    }
-    Vec<TO, N> o;
-    if (base) {
-        const Vec<TO, N> b = *reinterpret_cast<const Vec<TO, N>*>(base + (long long)t * H + c);
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += to_f(b.v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) o.v[i] = from_f<TO>(acc[i]);
-    *reinterpret_cast<Vec<TO, N>*>(y + (long long)t * H + c) = o;
-}
+// A thread takes N neighbouring elements of a token: the k rows' loads are issued
+// together (ROWS at a time), then added in the order of j.  Bound by memory: each
+// row is read once, in pieces of 16 bytes a thread.
+constexpr int ROWS = 8;
+constexpr int COMBINE_CTAS = 3;   // CTAs per SM: 24 warps with 8 rows in flight each
 
 template <typename TI, typename TO, int N>
-__global__ void __launch_bounds__(256) combine_backward_kernel(const TO* __restrict__ dy, const TI* __restrict__ ys,
-                                                               int T, int H, const int32_t* __restrict__ pos, int k,
-                                                               const float* __restrict__ w, TI* __restrict__ dys,
-                                                               float* __restrict__ dw) {
-    __shared__ float part[8];
+__global__ void __launch_bounds__(256, COMBINE_CTAS) combine_kernel(const TI* __restrict__ ys, int T, int H,
+                                                          const int32_t* __restrict__ pos, int k,
+                                                          const float* __restrict__ w, const TO* base, TO* y) {
+    const int per = H / N;                                     // pieces of a row
+    const unsigned long long R = (unsigned long long)T * k;
+    // the thread's first piece, and how far it is to the next (in tokens and pieces)
+    const long long item = (long long)blockIdx.x * 256 + threadIdx.x, step = (long long)gridDim.x * 256;
+    long long t = item / per;
+    int c = (int)(item - t * per);
+    const long long dt = step / per;
+    const int dc = (int)(step - dt * per);
     grid_dep_launch();
     grid_dep_wait();
-    const int t = blockIdx.x;
-    const long long R = (long long)T * k;
-    for (int j = 0; j < k; ++j) {
-        const int at = pos[(long long)t * k + j];
-        const bool live = (unsigned long long)(long long)at < (unsigned long long)R;
-        float s = 0.f;
-        if (live) {
-            const float wj = w[(long long)t * k + j];
-            for (int c = threadIdx.x * N; c < H; c += 256 * N) {
-                const Vec<TO, N> d = *reinterpret_cast<const Vec<TO, N>*>(dy + (long long)t * H + c);
-                const Vec<TI, N> v = *reinterpret_cast<const Vec<TI, N>*>(ys + (long long)at * H + c);
-                Vec<TI, N> o;
+    int at[ROWS];
+    auto places = [&](long long t, int j0) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    s = fmaf(to_f(d.v[i]), to_f(v.v[i]), s);
-                    o.v[i] = from_f<TI>(wj * to_f(d.v[i]));
+        for (int j = 0; j < ROWS; ++j) {
+            const long long r = t < T && j0 + j < k ? pos[t * k + j0 + j] : -1;
+            at[j] = (unsigned long long)r < R ? (int)r : -1;
+        }
+    };
+    places(t, 0);
+    while (t < T) {
+        float acc[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = 0.f;
+        const long long here = t * H + (long long)c * N;
+        long long tn = t + dt;
+        int cn = c + dc;
+        if (cn >= per) {
+            cn -= per;
+            ++tn;
+        }
+        for (int j0 = 0; j0 < k; j0 += ROWS) {
+            float wj[ROWS];
+            Vec<TI, N> v[ROWS];
+            unsigned live = 0;
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j)
+                if (at[j] >= 0) {
+                    v[j] = *reinterpret_cast<const Vec<TI, N>*>(ys + (long long)at[j] * H + c * N);
+                    wj[j] = w ? w[t * k + j0 + j] : 1.f;
+                    live |= 1u << j;
                 }
-                *reinterpret_cast<Vec<TI, N>*>(dys + (long long)at * H + c) = o;
-            }
+            // the places of the next rows come while these are on their way
+            if (j0 + ROWS < k) places(t, j0 + ROWS);
+            else places(tn, 0);
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j)
+                if (live >> j & 1u)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[i] = fmaf(wj[j], to_f(v[j].v[i]), acc[i]);
+        }
+        Vec<TO, N> o;
+        if (base) {
+            const Vec<TO, N> b = *reinterpret_cast<const Vec<TO, N>*>(base + here);
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] += to_f(b.v[i]);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float z = 0.f;
-            for (int i = 0; i < 8; ++i) z += part[i];
-            dw[(long long)t * k + j] = z;
+        for (int i = 0; i < N; ++i) o.v[i] = from_f<TO>(acc[i]);
+        *reinterpret_cast<Vec<TO, N>*>(y + here) = o;
+        t = tn;
+        c = cn;
+    }
+}
+
+// One CTA per token; a thread reads its pieces of dy once for all k rows.  The k dot
+// products are summed per thread, then over the warp and the warps in a fixed order.
+template <typename TI, typename TO, int N>
+__global__ void __launch_bounds__(256, 2) combine_backward_kernel(const TO* __restrict__ dy, const TI* ys, int T, int H,
+                                                               const int32_t* __restrict__ pos, int k,
+                                                               const float* __restrict__ w, TI* dys,
+                                                               float* __restrict__ dw) {
+    __shared__ float part[8][16];
+    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const unsigned long long R = (unsigned long long)T * k;
+    grid_dep_launch();
+    grid_dep_wait();
+    pos += (long long)t * k;
+    w += (long long)t * k;
+    dy += (long long)t * H;
+    for (int j0 = 0; j0 < k; j0 += ROWS) {
+        long long at[ROWS];
+        float wj[ROWS], s[ROWS];
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+            const long long r = j0 + j < k ? pos[j0 + j] : -1;
+            at[j] = (unsigned long long)r < R ? r * H : -1;
+            wj[j] = j0 + j < k ? w[j0 + j] : 0.f;
+            s[j] = 0.f;
         }
-        __syncthreads();
+        for (int c = threadIdx.x * N; c < H; c += blockDim.x * N) {
+            const Vec<TO, N> d = *reinterpret_cast<const Vec<TO, N>*>(dy + c);
+            Vec<TI, N> v[ROWS];
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j)
+                if (at[j] >= 0) v[j] = *reinterpret_cast<const Vec<TI, N>*>(ys + at[j] + c);
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j)
+                if (at[j] >= 0) {
+                    Vec<TI, N> o;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        s[j] = fmaf(to_f(d.v[i]), to_f(v[j].v[i]), s[j]);
+                        o.v[i] = from_f<TI>(wj[j] * to_f(d.v[i]));
+                    }
+                    *reinterpret_cast<Vec<TI, N>*>(dys + at[j] + c) = o;
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+            if (lane == 0) part[warp][(j0 + j) & 15] = s[j];
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < k) {
+        float z = 0.f;
+        for (int i = 0; i < warps; ++i) z += part[i][threadIdx.x];
+        dw[(long long)t * k + threadIdx.x] = z;
     }
 }
 
@@ -289,45 +415,66 @@ __global__ void __launch_bounds__(256) router_backward_kernel(const int32_t* __r
         const float dj = __shfl_sync(0xffffffffu, d, j);
         if (ej == e) sum += dj;
     }
-    for (int i = lane; i < E; i += 32) out[i] = 0.f;
+    if ((E & 3) == 0 && ((uintptr_t)dlogits & 15u) == 0)
+        for (int i = lane; i < E / 4; i += 32) reinterpret_cast<float4*>(out)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    else
+        for (int i = lane; i < E; i += 32) out[i] = 0.f;
     __syncwarp();
     if (lane < k && (unsigned)e < (unsigned)E) out[e] = sum;
+}
+
+// Elements a thread takes at a time: 16 bytes of a row where rows and pointers allow,
+// else two elements, else one.
+template <typename TI, typename TO>
+int piece(uintptr_t all, uintptr_t rows, uintptr_t outs, int H) {
+    constexpr int N = 16 / sizeof(TI);
+    if (H % N == 0 && (all & 15u) == 0) return N;
+    return H % 2 == 0 && (rows & (2 * sizeof(TI) - 1)) == 0 && (outs & (2 * sizeof(TO) - 1)) == 0 ? 2 : 1;
 }
 
 template <typename TI, typename TO>
 cudaError_t combine_t(const void* ys, int T, int H, const int32_t* pos, int k, const float* w, const void* base,
                       void* y, cudaStream_t stream) {
-    constexpr int N = 8;
-    const uintptr_t a = (uintptr_t)ys | (uintptr_t)base | (uintptr_t)y;
-    if (H % N == 0 && (a & 15u) == 0) {
-        const int bpr = (H / N + 255) / 256;
-        return launch_dependent(combine_kernel<TI, TO, N>, (unsigned)T * bpr, 256, 0, stream, (const TI*)ys, T, H, pos,
-                                k, w, (const TO*)base, (TO*)y, bpr);
-    }
-    const int bpr = (H + 255) / 256;
-    return launch_dependent(combine_kernel<TI, TO, 1>, (unsigned)T * bpr, 256, 0, stream, (const TI*)ys, T, H, pos, k,
-                            w, (const TO*)base, (TO*)y, bpr);
+    const int n = piece<TI, TO>((uintptr_t)ys | (uintptr_t)base | (uintptr_t)y, (uintptr_t)ys, (uintptr_t)base | (uintptr_t)y, H);
+    const long long items = (long long)T * (H / n);
+    int sms = 0;
+    cudaError_t e = device_sms(sms);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)std::min<long long>((items + 255) / 256, (long long)sms * COMBINE_CTAS);
+    auto kernel = n == 1 ? combine_kernel<TI, TO, 1> : n == 2 ? combine_kernel<TI, TO, 2> : combine_kernel<TI, TO, 16 / sizeof(TI)>;
+    return launch_dependent(kernel, grid, 256, 0, stream, (const TI*)ys, T, H, pos, k, w, (const TO*)base, (TO*)y);
 }
 
 template <typename TI, typename TO>
 cudaError_t combine_backward_t(const void* dy, const void* ys, int T, int H, const int32_t* pos, int k, const float* w,
                                void* dys, float* dw, cudaStream_t stream) {
-    constexpr int N = 8;
-    const uintptr_t a = (uintptr_t)ys | (uintptr_t)dy | (uintptr_t)dys;
-    if (H % N == 0 && (a & 15u) == 0)
-        return launch_dependent(combine_backward_kernel<TI, TO, N>, (unsigned)T, 256, 0, stream, (const TO*)dy,
-                                (const TI*)ys, T, H, pos, k, w, (TI*)dys, dw);
-    return launch_dependent(combine_backward_kernel<TI, TO, 1>, (unsigned)T, 256, 0, stream, (const TO*)dy,
-                            (const TI*)ys, T, H, pos, k, w, (TI*)dys, dw);
+    const int n = piece<TI, TO>((uintptr_t)ys | (uintptr_t)dy | (uintptr_t)dys, (uintptr_t)ys | (uintptr_t)dys, (uintptr_t)dy, H);
+    const unsigned block = (unsigned)std::min(256, (H / n + 31) / 32 * 32);
+    auto kernel = n == 1   ? combine_backward_kernel<TI, TO, 1>
+                  : n == 2 ? combine_backward_kernel<TI, TO, 2>
+                           : combine_backward_kernel<TI, TO, 16 / sizeof(TI)>;
+    return launch_dependent(kernel, (unsigned)T, block, 0, stream, (const TO*)dy, (const TI*)ys, T, H, pos, k, w, (TI*)dys, dw);
 }
 
 }  // namespace
 
+// One slice per SM: the grouping of a slice is one CTA's work.
 int group_slices(int T, int k) {
     (void)k;
-    return std::min(T, 296);
+    return std::min(T, 148);
 }
 bool group_two_launches(int T, int k) { return (long long)T * k > GROUP_ONE; }
+
+namespace {
+template <bool BULK, typename V>
+cudaError_t group_place(const GroupParams& p, bool two, cudaStream_t stream) {
+    const int smem = BULK ? GROUP_SMEM : 0;
+    static SmemLimit limit[2];
+    auto kernel = two ? group_place_kernel<false, BULK, V> : group_place_kernel<true, BULK, V>;
+    cudaError_t e = BULK ? limit[two].ensure((const void*)kernel, smem) : cudaSuccess;
+    return e != cudaSuccess ? e : launch_dependent(kernel, p.slices, GT, smem, stream, p);
+}
+}  // namespace
 
 cudaError_t group_launch(const GroupParams& p0, cudaStream_t stream) {
     GroupParams p = p0;
@@ -340,14 +487,11 @@ cudaError_t group_launch(const GroupParams& p0, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     const uintptr_t a = (uintptr_t)p.x | (uintptr_t)p.xs | (uintptr_t)p.row_bytes;
-    if ((a & 15u) == 0)
-        return two ? launch_dependent(group_place_kernel<false, uint4>, p.slices, GT, 0, stream, p)
-                   : launch_dependent(group_place_kernel<true, uint4>, p.slices, GT, 0, stream, p);
-    if ((a & 3u) == 0)
-        return two ? launch_dependent(group_place_kernel<false, uint32_t>, p.slices, GT, 0, stream, p)
-                   : launch_dependent(group_place_kernel<true, uint32_t>, p.slices, GT, 0, stream, p);
-    return two ? launch_dependent(group_place_kernel<false, uint16_t>, p.slices, GT, 0, stream, p)
-               : launch_dependent(group_place_kernel<true, uint16_t>, p.slices, GT, 0, stream, p);
+    // bulk stores for the longer batches; for a few tokens all threads of a CTA copy a row (T = 4, k = 6, rows of
+    // 8 KB: 2.95 us against 3.2 by bulk stores)
+    if (p.x && (a & 15u) == 0)
+        return two ? group_place<true, uint4>(p, two, stream) : group_place<false, uint4>(p, two, stream);
+    return (a & 3u) == 0 ? group_place<false, uint32_t>(p, two, stream) : group_place<false, uint16_t>(p, two, stream);
 }
 
 cudaError_t combine_launch(const void* ys, int dtype, int T, int H, const int32_t* pos, int k, const float* w,
