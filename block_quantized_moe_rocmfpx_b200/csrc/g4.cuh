@@ -216,115 +216,90 @@ __device__ __forceinline__ float g4_silu_mul(float g, float u) {
     return g < -64.f ? silu_mul_tail(g, u) : g / (1.f + expf(-g)) * u;
 }
 
-// The experts with rows, read once per CTA: the i-th is expert e[i] with rows lo[i] ..
-// hi[i] and blk[i] slots (passes of p.cols rows) before it.
+// A value that is the same in all lanes, told to the compiler (it then lives in a
+// uniform register and its branches need no reconvergence).
+__device__ __forceinline__ int g4_uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Rows of x by expert, read once per CTA: blk[e] slots (passes of p.cols = 1 << p.shift
+// rows) before expert e, and its rows lo[e] .. hi[e].
 struct G4Rows {
     int32_t blk[G4_MAXE + 1];
-    int32_t e[G4_MAXE], lo[G4_MAXE], hi[G4_MAXE];
-    int32_t count;
-    int2 wsum[32];
+    int32_t lo[G4_MAXE], hi[G4_MAXE];
+    int32_t wsum[32];
 };
 
 template <int WARPS>
 __device__ __forceinline__ int g4_rows(G4Rows& s, const G4Params& p) {
     constexpr int PER = (G4_MAXE + 32 * WARPS - 1) / (32 * WARPS);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int lo[PER], hi[PER], n[PER];
-    int2 sum = {0, 0};   // experts, slots
+    int n[PER], sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = PER * tid + i;
-        lo[i] = hi[i] = 0;
+        n[i] = 0;
         if (e < p.E) {
-            lo[i] = max(0, min(p.offsets[e], p.R));
-            hi[i] = max(lo[i], min(p.offsets[e + 1], p.R));
+            const int lo = max(0, min(p.offsets[e], p.R)), hi = max(lo, min(p.offsets[e + 1], p.R));
+            s.lo[e] = lo;
+            s.hi[e] = hi;
+            n[i] = (hi - lo + p.cols - 1) >> p.shift;
         }
-        n[i] = (hi[i] - lo[i] + p.cols - 1) / p.cols;
-        sum.x += n[i] > 0;
-        sum.y += n[i];
+        sum += n[i];
     }
-    const int2 own = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, sum.x, o), y = __shfl_up_sync(0xffffffffu, sum.y, o);
-        if (lane >= o) {
-            sum.x += x;
-            sum.y += y;
+    const int own = sum;
+    auto scan = [&](int v) {
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
         }
-    }
+        return v;
+    };
+    sum = scan(sum);
     if (lane == 31) s.wsum[warp] = sum;
     __syncthreads();
-    int2 at = {sum.x - own.x, sum.y - own.y}, all = {0, 0};
+    const int sums = scan(lane < WARPS ? s.wsum[lane] : 0);
+    int at = sum - own + (warp ? __shfl_sync(0xffffffffu, sums, warp - 1) : 0);
+    const int all = __shfl_sync(0xffffffffu, sums, 31);
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        const int2 v = s.wsum[w];
-        if (w < warp) {
-            at.x += v.x;
-            at.y += v.y;
-        }
-        all.x += v.x;
-        all.y += v.y;
+    for (int i = 0; i < PER; ++i) {
+        if (PER * tid + i <= p.E) s.blk[PER * tid + i] = at;
+        at += n[i];
     }
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (n[i] > 0) {
-            s.blk[at.x] = at.y;
-            s.e[at.x] = PER * tid + i;
-            s.lo[at.x] = lo[i];
-            s.hi[at.x] = hi[i];
-            ++at.x;
-            at.y += n[i];
-        }
-    if (tid == 0) {
-        s.blk[all.x] = all.y;
-        s.count = all.x;
-    }
+    if (tid == 0) s.blk[p.E] = all;
     __syncthreads();
-    return all.y;
+    return all;
 }
 
-// A value that is the same in all lanes, told to the compiler (it then lives in a
-// uniform register and its branches need no reconvergence).
-__device__ __forceinline__ int g4_uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-
 // A unit: row-groups of a matrix against the columns of a slot (one pass over the
-// matrix of the i-th expert with rows).
+// matrix of expert e).
+template <bool EXPERTS>
 struct G4Walk {
-    int slot, unit, i;
-    __device__ __forceinline__ void start(int u, const G4Rows* s, const G4Params& p) {
-        slot = u / p.units;
-        unit = u % p.units;
-        i = p.offsets ? find(slot, s) : 0;
-    }
-    static __device__ __forceinline__ int find(int slot, const G4Rows* s) {   // the largest i with blk[i] <= slot
-        int i = 0;
-        for (int hi = s->count; hi - i > 1;) {
-            const int mid = (i + hi) >> 1;
-            if (s->blk[mid] <= slot) i = mid;
+    int slot, unit, e;
+    static __device__ __forceinline__ int find(int slot, const G4Rows* s, const G4Params& p) {
+        if constexpr (!EXPERTS) return 0;
+        int e = 0;          // the largest e with blk[e] <= slot
+#pragma unroll 1
+        for (int hi = p.E; hi - e > 1;) {
+            const int mid = (e + hi) >> 1;
+            if (s->blk[mid] <= slot) e = mid;
             else hi = mid;
         }
-        return i;
+        return e;
     }
     __device__ __forceinline__ void step(int by, const G4Rows* s, const G4Params& p) {
         unit += by;
-        if (unit < p.units) return;
+        if (!EXPERTS || unit < p.units) return;
         do {
             unit -= p.units;
             ++slot;
         } while (unit >= p.units);
-        if (p.offsets) {
-            while (i + 1 < s->count && s->blk[i + 1] <= slot) ++i;
-            i = g4_uniform(i);
-        }
-    }
-    __device__ __forceinline__ long long expert(const G4Rows* s, const G4Params& p) const {
-        return p.offsets ? g4_uniform(s->e[i]) : 0;
+        e = g4_uniform(find(slot, s, p));
     }
     __device__ __forceinline__ int row(const G4Rows* s, const G4Params& p) const {
-        return p.offsets ? s->lo[i] + p.cols * (slot - s->blk[i]) : 0;
+        return EXPERTS ? s->lo[e] + ((slot - s->blk[e]) << p.shift) : 0;
     }
     __device__ __forceinline__ int cols(const G4Rows* s, const G4Params& p, int row) const {
-        return min(p.cols, (p.offsets ? s->hi[i] : p.R) - row);
+        return EXPERTS ? min(p.cols, s->hi[e] - row) : p.R;
     }
 };
 
@@ -339,36 +314,50 @@ struct G4Phase {
     int slot_col[G4_COLS], slot_prod[G4_COLS];   // of a slot: its first column and product
 };
 
-// As many slots from `first` on as there is room for, up to `last`: one warp, a lane per
-// slot.
-template <int XT, int G>
-__device__ __forceinline__ void g4_plan(G4Phase& ph, int first, int last, const G4Rows* s, const G4Params& p) {
+// As many slots from `first` on as there is room for, up to the one of unit u1 - 1: one
+// warp, a lane per slot.  (One matrix: its only slot.)
+template <int XT, int G, bool EXPERTS>
+__device__ __forceinline__ void g4_plan(G4Phase& ph, int first, int u1, const G4Rows* s, const G4Params& p) {
     constexpr int P = G4X<XT>::PARTS, CO = G4X<XT>::COLS;
     const int lane = threadIdx.x & 31;
-    G4Walk f = {first + lane, 0, 0};
+    if constexpr (!EXPERTS) {
+        if (lane < p.R) {
+            ph.row[lane] = lane;
+            ph.sum[lane] = lane / CO * 8 + lane % CO * (8 / CO);
+            ph.top[lane] = 0;
+        }
+        if (lane == 0) {
+            ph.end = 1;
+            ph.cols = p.R;
+            ph.products = (p.R + CO - 1) / CO + 1;
+            ph.slot_col[0] = ph.slot_prod[0] = 0;
+        }
+        return;
+    }
+    const int slot = first + lane;
+    const bool in = (long long)slot * p.units < u1;
     int row = 0, c = 0;
-    if (f.slot <= last) {
-        if (p.offsets) f.i = G4Walk::find(f.slot, s);
+    if (in) {
+        const G4Walk<true> f = {slot, 0, G4Walk<true>::find(slot, s, p)};
         row = f.row(s, p);
         c = f.cols(s, p, row);
     }
     const int q = (c + CO - 1) / CO;
-    int cols = c, products = q;
-#pragma unroll
+    int both = c | q << 16;   // at most 32 * 8 of either
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, cols, o), y = __shfl_up_sync(0xffffffffu, products, o);
-        if (lane >= o) {
-            cols += x;
-            products += y;
-        }
+        const int x = __shfl_up_sync(0xffffffffu, both, o);
+        if (lane >= o) both += x;
     }
+    const int cols = both & 0xFFFF, products = both >> 16;
     // a second product may be read where a slot has only one
-    const bool fits = f.slot <= last && (lane == 0 || (cols <= G4_COLS && (p.c1 - p.c0) * g4_x_bytes(G, products + 1, cols * P) <= p.x_room));
+    const bool fits = in && (lane == 0 || (cols <= G4_COLS && (p.c1 - p.c0) * g4_x_bytes(G, products + 1, cols * P) <= p.x_room));
     const unsigned no = ~__ballot_sync(0xffffffffu, fits);
     const int n = no ? __ffs(no) - 1 : 32;
     if (lane < n) {
         ph.slot_col[lane] = cols - c;
         ph.slot_prod[lane] = products - q;
+#pragma unroll 1
         for (int j = 0; j < c; ++j) {
             ph.row[cols - c + j] = row + j;
             ph.sum[cols - c + j] = (products - q + j / CO) * 8 + j % CO * (8 / CO);
@@ -454,10 +443,13 @@ __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, uint8
 // and are added in warp order.  That is put off until the team's buffer is full (8 units
 // of one column, 1 of 8), so that the warps of a team wait for one another as rarely
 // as they can.
-template <int XT, int G, bool Z, bool PAIR, int NBMAX>
+// MODE: 0 one matrix, 1 experts, 2 gate and up of experts (PAIR)
+template <int XT, int G, bool Z, int MODE, int NBMAX>
 __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p) {
     constexpr int FULL = g4_chunk_bytes(G4_CHUNK, G, Z);
     constexpr int P = G4X<XT>::PARTS, WARPS = g4_warps(NBMAX);
+    constexpr bool EXPERTS = MODE > 0, PAIR = MODE == 2;
+    using Walk = G4Walk<EXPERTS>;
     constexpr int STAGE = G4_NR * FULL, RING = 2 * STAGE;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int2 wait_all[WARPS][8];   // (unit, row of y) of the blocks of 32 sums that wait
@@ -467,34 +459,38 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
     uint8_t* const xs = smem + WARPS * 1024 + WARPS * RING;
     G4Rows* const rows = reinterpret_cast<G4Rows*>(xs + p.x_room);
     const int lane = threadIdx.x & 31, warp = g4_uniform(threadIdx.x >> 5);
-    const int team = warp / p.team, member = warp % p.team, teams = WARPS / p.team;
+    const int team = warp * p.inv_team >> 16, member = warp - team * p.team, teams = p.teams;
     float* const red = red_all + team * p.team * 256;
     const int chunks = p.c1 - p.c0;
     grid_dep_launch();
     grid_dep_wait();
-    const int slots = p.offsets ? g4_uniform(g4_rows<WARPS>(*rows, p)) : 1;
-    const int total = slots * p.units;
-    const int u0 = (int)((long long)total * blockIdx.x / gridDim.x), u1 = (int)((long long)total * (blockIdx.x + 1) / gridDim.x);
+    const int slots = EXPERTS ? g4_uniform(g4_rows<WARPS>(*rows, p)) : 1;
+    // the CTA's units u0 .. u1 - 1
+    const int total = slots * p.units, b = blockIdx.x, each = total / gridDim.x, more = total - each * gridDim.x;
+    const int u0 = each * b + min(b, more), u1 = u0 + each + (b < more);
     if (u0 == u1) return;
 
     // loads: the next chunk of this warp, in order
-    G4Walk w;
-    w.start(min(u0 + team, total - 1), rows, p);
+    Walk w;
+    const int first_slot = EXPERTS ? u0 / p.units : 0;
+    w.slot = first_slot;
+    w.unit = u0 - first_slot * p.units;
+    w.e = g4_uniform(Walk::find(w.slot, rows, p));
+    if (team) w.step(team, rows, p);
     const uint8_t* const ring = smem + WARPS * 1024 + warp * RING;
     const uint32_t ring_s = smem_u32(ring) + lane * 16;
     const int o_tail = (lane >> 4) * (FULL - 256) + 1024;              // the lane's piece behind the codes of either row-group
     const bool has_tail = (lane & 15) * 16 < FULL - 1024;
     // the warp's chunks of a unit; the last of them may be the short end of K
-    const int n = g4_uniform((chunks - member + p.team - 1) / p.team);
+    const int n = p.each + (member < p.more);
     const int last = p.K - (p.c0 + member + (n - 1) * p.team) * G4_CHUNK;
     const int end = last < G4_CHUNK ? 1 : 0;                           // chunks to go when the short one is next, 0: there is none
     const int jump = p.team * FULL;
-    int left = u0 + team < u1 ? (u1 - u0 - team + teams - 1) / teams : 0;   // units of this team
-    int fu = left, fl = left ? n : 0, fstage = 0;                      // units, chunks of the unit still to load
+    int fu = u0 + team, fl = fu < u1 ? n : 0, fstage = 0;               // unit and chunks of it still to load, 0: nothing left
     const uint8_t *f0 = nullptr, *f1 = nullptr, *f2 = nullptr;         // the lane's pieces: codes of both, and behind
-    G4Walk f = w;
+    Walk f = w;
     auto aim = [&]() {
-        const long long at = f.expert(rows, p) * p.stride + (long long)(p.c0 + member) * FULL;
+        const long long at = f.e * p.stride + (long long)(p.c0 + member) * FULL;
         const uint8_t *r0, *r1;
         if constexpr (PAIR) {
             r0 = p.W0 + at + f.unit * p.rg_bytes;
@@ -526,7 +522,7 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
             f0 += jump;
             f1 += jump;
             f2 += jump;
-            if (--fl == 0 && --fu > 0) {
+            if (--fl == 0 && (fu += teams) < u1) {
                 f.step(teams, rows, p);
                 fl = n;
                 aim();
@@ -614,18 +610,18 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
     };
     for (int u = u0 + team;;) {
         // x of the next slots, when the CTA is through with the last ones
-        first = phase_end < 0 ? u0 / p.units : phase_end;
-        if (warp == 0) g4_plan<XT, G>(ph, first, (u1 - 1) / p.units, rows, p);
+        first = phase_end < 0 ? first_slot : phase_end;
+        if (warp == 0) g4_plan<XT, G, EXPERTS>(ph, first, u1, rows, p);
         __syncthreads();
         phase_end = g4_uniform(ph.end);
         products = g4_uniform(ph.products);
         tile = g4_uniform(ph.cols) * P * 64;
         x_chunk = g4_x_bytes(G, products, g4_uniform(ph.cols) * P);
         g4_stage_x<XT, G, Z, WARPS>(p, ph, xs);
-        const bool done = phase_end * (long long)p.units >= u1;   // the CTA's last slots
+        const bool done = !EXPERTS || phase_end * (long long)p.units >= u1;   // the CTA's last slots
 #pragma unroll 1
         while (true) {
-            const bool more = u < u1 && w.slot < phase_end;
+            const bool more = u < u1 && (!EXPERTS || w.slot < phase_end);
             int row0 = 0, cols = 0;
             if (more) {
                 row0 = g4_uniform(w.row(rows, p));
@@ -633,7 +629,8 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
             }
             if (more ? used + cols > 8 : done && used) flush();
             if (!more) break;
-            const int col0 = g4_uniform(ph.slot_col[w.slot - first]), prod0 = g4_uniform(ph.slot_prod[w.slot - first]);
+            const int col0 = EXPERTS ? g4_uniform(ph.slot_col[w.slot - first]) : 0;
+            const int prod0 = EXPERTS ? g4_uniform(ph.slot_prod[w.slot - first]) : 0;
             if (NBMAX == 1 || cols <= 2) unit(std::integral_constant<int, 1>(), cols, col0, prod0);
             else unit(std::integral_constant<int, NBMAX>(), cols, col0, prod0);
             if (member == 0 && lane < cols) wait_all[team][used + lane] = make_int2(w.unit, row0 + lane);
@@ -663,65 +660,77 @@ inline int g4_team(long long units, int chunks, int sms, int warps) {
     return best;
 }
 
-template <int XT, int G, bool Z, bool PAIR, int NBMAX>
+template <int XT, int G, bool Z, int MODE, int NBMAX>
 cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
+    constexpr bool EXPERTS = MODE > 0, PAIR = MODE == 2;
     int sms = 0;
     cudaError_t e = device_sms(sms);
     if (e != cudaSuccess) return e;
     constexpr int P = G4X<XT>::PARTS, CO = G4X<XT>::COLS, WARPS = g4_warps(NBMAX);
     constexpr int FULL = g4_chunk_bytes(G4_CHUNK, G, Z);
-    const int fixed = WARPS * 1024 + WARPS * 2 * G4_NR * FULL + (p.offsets ? (int)sizeof(G4Rows) : 0);
+    const int fixed = WARPS * 1024 + WARPS * 2 * G4_NR * FULL + (EXPERTS ? (int)sizeof(G4Rows) : 0);
     const int room = (G4_SMEM - (int)sizeof(G4Phase) - WARPS * 64 - 512 - fixed) & ~127;   // less the kernel's static part
     p.rg_bytes = g4_rowgroup_bytes(p.K, G, Z);
     p.units = PAIR ? (p.N + 15) / 16 : (p.N + 31) / 32;
     const int chunks = (p.K + G4_CHUNK - 1) / G4_CHUNK;
     // columns of a pass: as many as there can be, with the x of all of K in shared memory.  Where that does not fit, fewer columns a pass (gate/up, whose sums have to be
     // whole before silu) or K in parts, one launch each (the weights are then still read once).
-    p.cols = std::min(p.R, NBMAX * CO);
+    // (Experts: a power of two, so that rows are counted by shifts.)
     int span = 0, x_chunk = 0;
+    for (p.shift = 0; EXPERTS && (1 << p.shift) < std::min(p.R, NBMAX * CO); ++p.shift) {}
+    p.cols = EXPERTS ? 1 << p.shift : std::min(p.R, NBMAX * CO);
     while (true) {
         x_chunk = g4_x_bytes(G, (p.cols + CO - 1) / CO + 1, p.cols * P);
         span = std::min(chunks, room / x_chunk);
         if (span == chunks || !PAIR || p.cols == 1) break;
-        --p.cols;
+        p.cols = 1 << --p.shift;
     }
     if (span < 1 || (PAIR && span < chunks)) return cudaErrorNotSupported;
     // one matrix has one slot; experts up to one per row, and room for several
-    p.x_room = p.offsets ? room : span * x_chunk;
-    p.team = g4_team((long long)p.units * (p.offsets ? std::min(p.E, p.R) : 1), span, sms, WARPS);
-    const long long total = (long long)p.units * (p.offsets ? p.R : 1);
+    p.x_room = EXPERTS ? room : span * x_chunk;
+    p.team = g4_team((long long)p.units * (EXPERTS ? std::min(p.E, p.R) : 1), span, sms, WARPS);
+    p.teams = WARPS / p.team;
+    p.inv_team = (65536 + p.team - 1) / p.team;   // warp / team = warp * inv_team >> 16 for fewer than 32 warps
+    const long long total = (long long)p.units * (EXPERTS ? p.R : 1);
     const int grid = (int)std::min<long long>(sms, total);
     const int smem = fixed + p.x_room;
-    auto kernel = g4_kernel<XT, G, Z, PAIR, NBMAX>;
+    auto kernel = g4_kernel<XT, G, Z, MODE, NBMAX>;
     static SmemLimit limit;   // one per instantiation
     e = limit.ensure((const void*)kernel, smem);
     const int all = p.R;
     for (int r = 0; r < all && e == cudaSuccess; r += p.R) {
-        if (!p.offsets) {   // one matrix: a launch serves p.cols columns
+        if (!EXPERTS) {   // one matrix: a launch serves p.cols columns
             p.R = std::min(p.cols, all - r);
             p.x = (const uint8_t*)p.x + (r ? (long long)p.cols * p.K * G4X<XT>::BYTES : 0);
             p.y += r ? (long long)p.cols * p.N : 0;
         }
         for (p.c0 = 0; p.c0 < chunks && e == cudaSuccess; p.c0 = p.c1) {
             p.c1 = std::min(chunks, p.c0 + span);
+            p.each = (p.c1 - p.c0) / p.team;
+            p.more = (p.c1 - p.c0) % p.team;
             e = launch_dependent(kernel, grid, WARPS * 32, smem, stream, p);
         }
     }
     return e;
 }
 
-template <int XT, int G, bool Z, bool PAIR>
+template <int XT, int G, bool Z, int MODE>
 cudaError_t g4_launch_p(const G4Params& p, cudaStream_t stream) {
     // fp32 x: two products a pass (4 columns) where there are that many columns to an expert
     if constexpr (XT == 1)
-        if (p.R > 2 * (p.offsets ? p.E : 1)) return g4_launch_n<XT, G, Z, PAIR, 2>(p, stream);
-    return g4_launch_n<XT, G, Z, PAIR, 1>(p, stream);
+        if (p.R > 2 * (MODE ? p.E : 1)) return g4_launch_n<XT, G, Z, MODE, 2>(p, stream);
+    return g4_launch_n<XT, G, Z, MODE, 1>(p, stream);
+}
+
+template <int XT, int G, bool Z>
+cudaError_t g4_launch_m(const G4Params& p, cudaStream_t stream) {
+    return p.W1 ? g4_launch_p<XT, G, Z, 2>(p, stream)
+                : p.offsets ? g4_launch_p<XT, G, Z, 1>(p, stream) : g4_launch_p<XT, G, Z, 0>(p, stream);
 }
 
 template <int XT, int G>
 cudaError_t g4_launch_g(const G4Params& p, bool zeros, cudaStream_t stream) {
-    if (p.W1) return zeros ? g4_launch_p<XT, G, true, true>(p, stream) : g4_launch_p<XT, G, false, true>(p, stream);
-    return zeros ? g4_launch_p<XT, G, true, false>(p, stream) : g4_launch_p<XT, G, false, false>(p, stream);
+    return zeros ? g4_launch_m<XT, G, true>(p, stream) : g4_launch_m<XT, G, false>(p, stream);
 }
 
 template <int XT>

@@ -18,8 +18,9 @@ struct G4Params {
     long long rg_bytes;       // bytes of a row-group
     int c0, c1;               // chunks of this launch; c0 > 0 adds to y
     int units;                // units of a matrix
-    int team;                 // warps that share a unit
-    int cols;                 // rows of x per pass over a matrix, at most
+    int team, teams, inv_team;   // warps that share a unit, such teams in a CTA, 65536 / team
+    int each, more;           // chunks of a warp, and how many warps of a team have one more
+    int cols, shift;          // rows of x per pass over a matrix, at most (experts: 1 << shift)
     int x_room;               // shared memory for x
 };
 
