@@ -644,14 +644,16 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
 }
 
 // Warps per unit: the least time of the busiest team, a unit costing its chunks and
-// about one chunk more (walking, adding up).
+// about one and a half more (walking, adding up).  Measured with every team size (us, teams of
+// 24 / 12 / 8 / 6 / 4 / 3 / 2 warps): 131072 x 4096, G = 64, zeros, q = 4: 88 / 70 / 65 / 64 /
+// 62 / 62 / 64; 37 experts of 4096 x 2048, G = 32, fp32 x: 78 / 62 / 53 / 52 / 48 / 48 / 46.
 inline int g4_team(long long units, int chunks, int sms, int warps) {
     int best = warps;
     long long cost = -1;
     for (int s = warps; s >= 1; --s) {
         if (warps % s || (s > 1 && warps / s > 15)) continue;   // a named barrier per team
         const long long teams = (long long)sms * (warps / s);
-        const long long c = (units + teams - 1) / teams * ((chunks + s - 1) / s + 1);
+        const long long c = (units + teams - 1) / teams * (2 * ((chunks + s - 1) / s) + 3);
         if (cost < 0 || c < cost) {
             cost = c;
             best = s;

@@ -20,7 +20,7 @@ namespace {
 
 constexpr int GT = 512;          // threads of a grouping CTA
 constexpr int GROUP_MAXE = 1024;
-constexpr int GROUP_BATCH = 512; // entries placed per batch
+constexpr int GROUP_BATCH = GT;  // entries placed per batch, one per thread
 constexpr int GROUP_ONE = 4096;  // entries up to which every CTA counts all of idx itself
 
 // ------------------------------------------------------------- grouping ---
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(GT) group_place_kernel(GroupParams p) {
     __shared__ __align__(16) int32_t tot[GROUP_MAXE];
     __shared__ __align__(16) int32_t cur[GROUP_MAXE];
     __shared__ int32_t wsum[GT / 32];
-    __shared__ int32_t s_pos[GROUP_BATCH];   // a batch's expert ids, then its places
+    __shared__ int32_t s_pos[GROUP_BATCH];   // places of a batch's entries
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dep_launch();
     for (int e = tid; e < GROUP_MAXE; e += GT) {
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(GT) group_place_kernel(GroupParams p) {
     const int t1 = min(t0 + p.per, p.T);
     const long long first = (long long)t0 * p.k;
     const int tb = GROUP_BATCH / p.k;   // tokens per batch
-    for (int i = tid; i < min(tb, t1 - t0) * p.k; i += GT) s_pos[i] = p.idx[first + i];
+    int next = tid < min(tb, t1 - t0) * p.k ? p.idx[first + tid] : -1;   // the thread's entry of the next batch
     if constexpr (ONE) {
         for (long long i = tid; i < n; i += GT) {
             const int e = p.idx[i];
@@ -132,11 +132,20 @@ __global__ void __launch_bounds__(GT) group_place_kernel(GroupParams p) {
         const int q = tid % quads, l = tid / quads;
         if (l < lines) {
             int4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-#pragma unroll 10
-            for (int s = l; s < p.slices; s += lines) {
-                const int4 v = *reinterpret_cast<const int4*>(p.part + (long long)s * pitch + 4 * q);
-                a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-                if (s < (int)blockIdx.x) { b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w; }
+            for (int s0 = l; s0 < p.slices; s0 += 10 * lines) {
+                int4 v[10];   // all on their way at once
+#pragma unroll
+                for (int i = 0; i < 10; ++i) {
+                    const int s = s0 + i * lines;
+                    v[i] = make_int4(0, 0, 0, 0);
+                    if (s < p.slices) v[i] = __ldcg(reinterpret_cast<const int4*>(p.part + (long long)s * pitch) + q);
+                }
+#pragma unroll
+                for (int i = 0; i < 10; ++i) {
+                    const int4 u = v[i];
+                    a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
+                    if (s0 + i * lines < (int)blockIdx.x) { b.x += u.x; b.y += u.y; b.z += u.z; b.w += u.w; }
+                }
             }
             atomicAdd(&tot[4 * q + 0], a.x); atomicAdd(&tot[4 * q + 1], a.y);
             atomicAdd(&tot[4 * q + 2], a.z); atomicAdd(&tot[4 * q + 3], a.w);
@@ -171,39 +180,31 @@ __global__ void __launch_bounds__(GT) group_place_kernel(GroupParams p) {
     __syncthreads();
     for (int ta = t0; ta < t1; ta += tb) {
         const int nt = min(tb, t1 - ta);
-        if (ta > t0) {
-            for (int i = tid; i < nt * p.k; i += GT) s_pos[i] = p.idx[(long long)ta * p.k + i];
-            __syncthreads();
-        }
-        if (warp == 0) {
-            // 32 entries a step: lanes of one expert rank themselves by lane
-            bool bad = false;
-            for (int i = 0; i < nt * p.k; i += 32) {
-                const int m = i + lane;
-                const long long ent = (long long)ta * p.k + m;
-                int e = -1;
-                if (m < nt * p.k) {
-                    e = s_pos[m];
-                    if ((unsigned)e >= (unsigned)p.E) {
-                        bad |= e != -1;
-                        e = -1;
-                    }
-                }
-                const unsigned same = __match_any_sync(0xffffffffu, e);
-                const int rank = __popc(same & ((1u << lane) - 1u));
-                int at = -1;
+        // an entry per thread: lanes of one expert rank themselves by lane, the warps take their turns
+        const int m = nt * p.k;
+        const long long ent = (long long)ta * p.k + tid;
+        int e = next;
+        const bool bad = tid < m && e != -1 && (unsigned)e >= (unsigned)p.E;
+        if (tid >= m || bad) e = -1;
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.ctrl + MOE_CTRL_ERR, MOE_ERR_EXPERT);
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        const int rank = __popc(same & ((1u << lane) - 1u));
+        int at = -1;
+        for (int w = 0; w < (m + 31) >> 5; ++w) {
+            if (warp == w) {
                 if (e >= 0) at = cur[e] + rank;
                 __syncwarp();
                 if (e >= 0 && rank == 0) cur[e] += __popc(same);
-                __syncwarp();
-                if (m < nt * p.k) {
-                    s_pos[m] = at;
-                    p.pos[ent] = at;
-                    if (at >= 0) p.rows[at] = (int32_t)ent;
-                }
             }
-            if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.ctrl + MOE_CTRL_ERR, MOE_ERR_EXPERT);
+            __syncthreads();
         }
+        if (tid < m) {
+            s_pos[tid] = at;
+            p.pos[ent] = at;
+            if (at >= 0) p.rows[at] = (int32_t)ent;
+        }
+        const int tn = ta + tb;
+        if (tn < t1) next = tid < min(tb, t1 - tn) * p.k ? p.idx[(long long)tn * p.k + tid] : -1;
         __syncthreads();
         if constexpr (BULK) {
             group_copy(p, ta, nt, s_pos, ring);
