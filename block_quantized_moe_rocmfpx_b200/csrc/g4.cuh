@@ -447,7 +447,7 @@ __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, uint8
 template <int XT, int G, bool Z, int MODE, int NBMAX>
 __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p) {
     constexpr int FULL = g4_chunk_bytes(G4_CHUNK, G, Z);
-    constexpr int P = G4X<XT>::PARTS, WARPS = g4_warps(NBMAX);
+    constexpr int P = G4X<XT>::PARTS, XB = G4X<XT>::BYTES, WARPS = g4_warps(NBMAX);
     constexpr bool EXPERTS = MODE > 0, PAIR = MODE == 2;
     using Walk = G4Walk<EXPERTS>;
     constexpr int STAGE = G4_NR * FULL, RING = 2 * STAGE;
@@ -471,6 +471,10 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
     if (u0 == u1) return;
 
     // loads: the next chunk of this warp, in order
+    if constexpr (!EXPERTS) {   // the warp's first part of x, on its way while the rest is set up
+        const int k = (p.c0 + warp) * G4_CHUNK + 4 * lane;
+        if (k < p.K) asm volatile("prefetch.global.L1 [%0];" ::"l"((const uint8_t*)p.x + (long long)k * XB));
+    }
     Walk w;
     const int first_slot = EXPERTS ? u0 / p.units : 0;
     w.slot = first_slot;
@@ -651,7 +655,7 @@ inline int g4_team(long long units, int chunks, int sms, int warps) {
     int best = warps;
     long long cost = -1;
     for (int s = warps; s >= 1; --s) {
-        if (warps % s || (s > 1 && warps / s > 15)) continue;   // a named barrier per team
+        if (warps % s || warps / s > 15) continue;   // a named barrier per team
         const long long teams = (long long)sms * (warps / s);
         const long long c = (units + teams - 1) / teams * (2 * ((chunks + s - 1) / s) + 3);
         if (cost < 0 || c < cost) {
