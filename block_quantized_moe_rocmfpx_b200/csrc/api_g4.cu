@@ -46,8 +46,8 @@ int experts(const char* who, const void* W0, const void* W1, bool pair, size_t s
         return rfx_fail(RFX_EINVAL, std::string(who) + ": bad x_dtype");
     if (E < 1 || E > 1024 || R < 0) return rfx_fail(RFX_EINVAL, std::string(who) + ": need 1 <= E <= 1024 and R >= 0");
     if (pair && K > 12288) return rfx_fail(RFX_EUNSUPPORTED, std::string(who) + ": K <= 12288");
-    if ((N + 15) / 16 * R > 2147483647LL)
-        return rfx_fail(RFX_EUNSUPPORTED, std::string(who) + ": ceil(N / 16) * R must be below 2^31");
+    if ((N + 15) / 16 * R > 2147483000LL)   // units are counted in 32 bits, a team's step past the last included
+        return rfx_fail(RFX_EUNSUPPORTED, std::string(who) + ": ceil(N / 16) * R must be at most 2147483000");
     if (R == 0) return RFX_OK;
     if (!W0 || (pair && !W1) || !x || !offsets || !y) return rfx_fail(RFX_EINVAL, std::string(who) + ": null pointer");
     if (!aligned16(W0) || !aligned16(W1) || stride % 16 || !aligned16(x))

@@ -25,8 +25,8 @@ int check_rows(const char* who, int dtype, int T, int H, int k) {
     if (!dtype_ok(dtype)) return rfx_fail(RFX_EINVAL, std::string(who) + ": bad dtype");
     if (T < 0 || H < 1 || k < 1 || k > 16)
         return rfx_fail(RFX_EINVAL, std::string(who) + ": need T >= 0, H >= 1 and 1 <= k <= 16");
-    if ((long long)T * k > 2147483647LL || (long long)T * ((H + 255) / 256) > 2147483647LL)
-        return rfx_fail(RFX_EUNSUPPORTED, std::string(who) + ": T * k and T * ceil(H / 256) must be below 2^31");
+    if ((long long)T * k > 2147483647LL || H > (1 << 24))
+        return rfx_fail(RFX_EUNSUPPORTED, std::string(who) + ": T * k must be below 2^31 and H at most 2^24");
     return RFX_OK;
 }
 

@@ -9,12 +9,24 @@
 //   lie so that the half and the half turned by a byte have one at either place: a PRMT and
 //   four ANDs make eight operands of a word, and the x that meet codes at bits 7..10 are
 //   stored divided by 16.
-//   x: brought to max|x| in [2^13, 2^14) by a power of two (per column and warp's part
-//   of K) and rounded to fp16.  That keeps bf16 and fp16 values whole down to
-//   2^-23 of the largest, and 2^-35 of the largest below that.  fp32 x is cut into
-//   three such parts of 11 bits, which are columns of the product.
+//   x: brought to max|x| in [2^13, 2^14) by a power of two (per column, over the launch's
+//   part of K) and rounded to fp16.  That keeps bf16 and fp16 values whole down to
+//   2^-23 of the largest, and 2^-35 of the largest below that (fp32 sums keep 2^-24).
+//   fp32 x is cut into three such parts of 11 bits, which are columns of the product.
 //   zero: the sums start from -zero * sum_k x.
 // So the only roundings that count are the fp32 sums and the scale's product.
+//
+// Why mma.sync and not tcgen05: with 8 columns a 128 x 8 x 16 tcgen05.mma takes as long as one
+// with 128 columns (about 89 cycles, 23 weights a cycle and SM, where the weights arrive at 46),
+// its A operand would have to be written to shared memory decoded, and each group's sums read back from
+// tensor memory to be scaled.  Forms that were built and measured slower at 131072 x 4096 (G = 64,
+// zeros, q = 4; this one 61 us on the same kind of box): bf16 code - zero by subtraction, 79 us; e4m3 operands,
+// which mma.sync takes apart into fp16 ones, 107 us; weights straight into registers, two chunks ahead, 66 us, and with
+// an L2 prefetch of the next unit, 87 us; 16 or 32 warps instead of 24, 67 and 70 us; a third stage, 63 us.
+//
+// Bound at large sizes by memory (G = 128, q = 1: 4.8 TB/s of weights) with the instruction slots close
+// behind (G = 64, zeros, q = 4: 40 instructions per 16 x 32 weights, 68 % of the issue slots); at small ones by the
+// launch and its start (4 us for one 32 x 128 matrix).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,7 +45,6 @@ namespace {
 
 constexpr int G4_NR = 2;                        // row-groups a warp takes at a time
 constexpr int G4_MAXE = 1024;
-constexpr int G4_STAGES = 2;                    // chunk pairs of a warp's ring
 constexpr int G4_SMEM = 232448 - 1024;          // dynamic and static shared memory of a block, less what the system takes
 
 // x in shared memory, for the columns (rows of x) of one or more passes.  A row of
@@ -679,9 +690,10 @@ cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
     p.rg_bytes = g4_rowgroup_bytes(p.K, G, Z);
     p.units = PAIR ? (p.N + 15) / 16 : (p.N + 31) / 32;
     const int chunks = (p.K + G4_CHUNK - 1) / G4_CHUNK;
-    // columns of a pass: as many as there can be, with the x of all of K in shared memory.  Where that does not fit, fewer columns a pass (gate/up, whose sums have to be
-    // whole before silu) or K in parts, one launch each (the weights are then still read once).
-    // (Experts: a power of two, so that rows are counted by shifts.)
+    // columns of a pass: as many as there can be, with the x of all of K in shared memory.  Where that
+    // does not fit, fewer columns a pass (gate/up, whose sums have to be whole before silu) or K in
+    // parts, one launch each (the weights are then still read once).  (Experts: a power of two, so that
+    // rows are counted by shifts.)
     int span = 0, x_chunk = 0;
     for (p.shift = 0; EXPERTS && (1 << p.shift) < std::min(p.R, NBMAX * CO); ++p.shift) {}
     p.cols = EXPERTS ? 1 << p.shift : std::min(p.R, NBMAX * CO);

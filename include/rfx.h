@@ -213,8 +213,8 @@ int moe_router_topk_backward(const int32_t* idx, const float* w, const float* dw
  * moe_group_workspace_bytes(T, k, E) bytes, zeroed once with rfx_ws_init; calls
  * that overlap on the GPU must use different workspaces.  One launch, or two for
  * longer batches; no atomics on global memory, so the result is the same every time.
- * Limits: T >= 0, H >= 1, 1 <= E <= 1024, 1 <= k <= 16 (k may exceed E),
- * T * k < 2^31.  T = 0 is a no-op (offsets are not written).  Rows that are a
+ * Limits: T >= 0, 1 <= H <= 2^24, 1 <= E <= 1024, 1 <= k <= 16 (k may exceed E),
+ * T * k < 2^31 (T, H, k for the three calls below too).  T = 0 is a no-op (offsets are not written).  Rows that are a
  * multiple of 16 bytes at 16-byte aligned pointers are copied fastest; any H is accepted.
  */
 size_t moe_group_workspace_bytes(int T, int k, int E);
@@ -322,10 +322,16 @@ int rfx_g4_pack_device(const uint8_t* codes, const uint16_t* scales, const uint8
 /*
  * y[c][n] = sum_k W[n][k] x[c][k] for c < q: rfx_gemv_q for G4 weights.  W:
  * device, packed [N][K], 16-byte aligned.  x: device [q][K] of x_dtype, 16-byte
- * aligned.  y: device fp32 [q][N].  The products (code - zero) * x are exact for
- * every x_dtype and are summed in fp32 within a group; each group's sum is scaled and
- * added in fp32.  A non-finite x makes its column non-finite and no other.
- * Limits: 1 <= q <= 8, N >= 1, K % group == 0.  One launch, no workspace.
+ * aligned.  y: device fp32 [q][N].
+ * Numerics: x enters as fp16 after a power of two per column that brings its largest
+ * magnitude to [2^13, 2^14): bf16 and fp16 values are whole down to 2^-23 of the largest and
+ * within 2^-35 of the largest below that; fp32 values enter as three such parts (33 bits).
+ * The products code * x are exact; each group's sum, code * x minus zero * sum of x, is taken in
+ * fp32, scaled and added in fp32.  The order of the sums depends on the shapes only, so results repeat bit for bit.
+ * A column of x with an infinity or a NaN gives NaN, and no other column does.
+ * Limits: 1 <= q <= 8, N >= 1, K % group == 0.  No workspace.  One launch; more where the
+ * columns' x does not fit shared memory (about q * K > 45,000 for 16-bit x, 14,000 for fp32) or fp32 x has more than
+ * 4 columns.
  */
 int rfx_gemv_g4(const void* W, int64_t N, int64_t K, int group, int has_zeros, const void* x, rfx_dtype x_dtype, int q,
                 float* y, void* stream);
@@ -339,9 +345,11 @@ int rfx_gemv_g4(const void* W, int64_t N, int64_t K, int group, int has_zeros, c
  * [R][K] of x_dtype, 16-byte aligned; offsets: device int32 [E + 1], ascending, read on the
  * device (values outside [0, R] are taken as the nearer end); y, h: device fp32
  * [R][N], rows outside every expert left as they were.  R: rows of x (T * k).
- * A pass over an expert's weights serves up to 8 of its rows; only experts with
- * rows are read.  Meant for decode and verify (few rows an expert).  Numerics as rfx_gemv_g4.  Limits:
- * 1 <= E <= 1024, R >= 0 (R = 0 is a no-op), N >= 1, K % group == 0.  One launch, no workspace.
+ * A pass over an expert's weights serves up to 8 of its rows (fp32 x: 2, or 4 where R > 2 E);
+ * only experts with rows are read.  Meant for decode and verify (few rows an expert).
+ * Numerics as rfx_gemv_g4; silu in fp32.  Limits: 1 <= E <= 1024, R >= 0 (R = 0 is a no-op), N >= 1,
+ * K % group == 0, ceil(N / 16) * R <= 2147483000, and K <= 12288 for moe_gate_up_g4.  No workspace; one launch (moe_gemv_g4:
+ * K in parts, a launch each, where x does not fit shared memory).
  */
 int moe_gemv_g4(const void* W, size_t stride, int E, int64_t N, int64_t K, int group, int has_zeros, const void* x,
                 rfx_dtype x_dtype, const int32_t* offsets, int R, float* y, void* stream);

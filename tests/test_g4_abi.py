@@ -131,6 +131,9 @@ def test_expert_product_refusals():
             assert f(**bad) == rfx.RFX_EINVAL, bad
         assert f(R=0, y=None) == rfx.RFX_OK
     assert pair(up=None) == rfx.RFX_EINVAL and pair(up=A + 8) == rfx.RFX_EINVAL
+    big = rfx.rfx_g4_packed_bytes(64, 12544, 64)
+    assert pair(K=12544, st=big) == rfx.RFX_EUNSUPPORTED
+    assert plain(N=2 ** 20, st=rfx.rfx_g4_packed_bytes(2 ** 20, 256, 64), R=2 ** 15) == rfx.RFX_EUNSUPPORTED
 
 
 def test_device_pack_refusals():

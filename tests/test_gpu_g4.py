@@ -11,11 +11,15 @@ times that for fp32 x, whose parts add up to at most 1.01 |x|) then stay below
 (K / G + 17) * 2^-24 * M; beside that bound the library's acceptance holds,
 relative L2 <= 1e-5.
 """
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import block_quantized_moe_rocmfpx_b200 as rfx
+from conftest import ROOT
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -243,6 +247,48 @@ def test_expert_products_many_experts_and_bad_offsets():
     y2 = torch.full((R, N), -5.0, device=DEV)
     rfx.moe_gemv_g4(packed, w.stride, N, K, G, x, off, y2)
     assert torch.equal(y2, y)
+
+
+@pytest.mark.parametrize("K,dtype,rows", [(64, BF, (8, 9)), (4096, HF, (7, 8)), (2048, FF, (1, 5))])
+def test_expert_products_of_many_passes(K, dtype, rows):
+    # a CTA meets more columns than fit shared memory at once: x comes in several turns
+    E, N, G = 300 if K > 64 else 1024, 32, 64
+    w = G4(N, K, G, True, 2, E=1, integer=True)
+    packed = w.packed.repeat(E)
+    counts = [rows[e % 2] for e in range(E)]
+    R = sum(counts)
+    x = x_of((R, K), dtype, 1, True)
+    y = torch.full((R, N), float("nan"), device=DEV)
+    rfx.moe_gemv_g4(packed, w.stride, N, K, G, x, offsets_of(counts), y, zeros=True)
+    check(y, w.dense(), x, G, integer=True)
+    h = torch.full((R, N), float("nan"), device=DEV)
+    rfx.moe_gate_up_g4(packed, packed, w.stride, N, K, G, x, offsets_of(counts), h, zeros=True)
+    a = x.double() @ w.dense().t()
+    want = a * torch.sigmoid(a) * a
+    # the products are exact: silu's division and exponential (2 ulp of it, |a| * 2^-24 * 2 of its argument) remain
+    bound = (6 + 2 * a.abs().clamp(max=104)) * 2.0 ** -23 * want.abs() + 1e-37
+    assert bool(((h.double() - want).abs() <= bound).all())
+
+
+def test_first_call_inside_a_capture():
+    # in a process of its own: nothing of the library has run before the capture
+    code = (
+        "import torch, block_quantized_moe_rocmfpx_b200 as rfx\n"
+        "d = 'cuda'\n"
+        "W = torch.zeros(rfx.rfx_g4_packed_bytes(64, 128, 64), dtype=torch.uint8, device=d)\n"
+        "x, y = torch.ones((1, 128), device=d).bfloat16(), torch.ones((1, 64), device=d)\n"
+        "pos, w = torch.zeros((1, 1), dtype=torch.int32, device=d), torch.ones((1, 1), device=d)\n"
+        "z = torch.zeros((1, 64), device=d)\n"
+        "g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    rfx.rfx_gemv_g4(W, 64, 128, 64, x, y)\n"
+        "    rfx.moe_combine_rows(y, pos, w, z)\n"
+        "z.fill_(5)\n"
+        "g.replay()\n"
+        "torch.cuda.synchronize()\n"
+        "assert (y == 0).all() and (z == 0).all()\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_python_checks_on_the_device():

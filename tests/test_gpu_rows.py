@@ -83,7 +83,7 @@ def check_group(x, idx_np, E):
 @pytest.mark.parametrize("dtype", [BF, HF, FF])
 @pytest.mark.parametrize("T,H,k,E", [(1, 8, 1, 1), (1, 4096, 6, 256), (4, 4096, 6, 256), (3, 1, 2, 5), (7, 33, 3, 4),
                                      (64, 250, 8, 9), (700, 72, 6, 300), (1500, 64, 8, 1024), (5000, 17, 2, 3),
-                                     (9001, 40, 4, 64)])
+                                     (9001, 40, 4, 64), (5, 8, 4, 2), (700, 2056, 6, 3)])
 def test_group_places_and_rows(T, H, k, E, dtype):
     rng = np.random.default_rng(T * 31 + H)
     x = torch.randn((T, H), device=DEV).to(dtype)

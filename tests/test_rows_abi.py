@@ -53,7 +53,8 @@ def test_combine_refusals():
                 {"ys": None}, {"pos": None}, {"w": None}, {"y": None}, {"ys": A + 1}, {"y": A + 2}, {"base": A + 2}):
         assert call(**bad) == rfx.RFX_EINVAL, bad
     assert call(T=0, y=None) == rfx.RFX_OK
-    assert call(T=2 ** 27, H=2 ** 13, k=1) == rfx.RFX_EUNSUPPORTED
+    assert call(H=2 ** 24 + 1) == rfx.RFX_EUNSUPPORTED
+    assert call(T=2 ** 30, k=2) == rfx.RFX_EUNSUPPORTED
 
 
 def test_combine_backward_refusals():
