@@ -45,6 +45,7 @@ namespace {
 
 constexpr int G4_NR = 2;                        // row-groups a warp takes at a time
 constexpr int G4_MAXE = 1024;
+constexpr int G4_SPLIT = 8;                     // CTAs of a cluster, at most
 constexpr int G4_SMEM = 232448 - 1024;          // dynamic and static shared memory of a block, less what the system takes
 
 // x in shared memory, for the columns (rows of x) of one or more passes.  A row of
@@ -81,24 +82,21 @@ __device__ __forceinline__ void g4_mma(float d[4], const uint32_t a[4], uint32_t
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// Four x values from k on, as fp32.
+// Four x values as they lie in memory, as fp32.
 template <int XT>
-__device__ __forceinline__ void g4_load_x(const uint8_t* x, float v[4]) {
+__device__ __forceinline__ void g4_x_values(uint4 q, float v[4]) {
     if constexpr (XT == 1) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(x));
-        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
+        v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
+    } else if constexpr (XT == 0) {
+        v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xFFFF0000u);
     } else {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(x));
-        if constexpr (XT == 0) {
-            v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xFFFF0000u);
-            v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xFFFF0000u);
-        } else {
-            __half2 a, b;
-            memcpy(&a, &q.x, 4);
-            memcpy(&b, &q.y, 4);
-            const float2 f = __half22float2(a), h = __half22float2(b);
-            v[0] = f.x; v[1] = f.y; v[2] = h.x; v[3] = h.y;
-        }
+        __half2 a, b;
+        memcpy(&a, &q.x, 4);
+        memcpy(&b, &q.y, 4);
+        const float2 f = __half22float2(a), h = __half22float2(b);
+        v[0] = f.x; v[1] = f.y; v[2] = h.x; v[3] = h.y;
     }
 }
 
@@ -328,7 +326,7 @@ struct G4Phase {
 // As many slots from `first` on as there is room for, up to the one of unit u1 - 1: one
 // warp, a lane per slot.  (One matrix: its only slot.)
 template <int XT, int G, bool EXPERTS>
-__device__ __forceinline__ void g4_plan(G4Phase& ph, int first, int u1, const G4Rows* s, const G4Params& p) {
+__device__ __forceinline__ void g4_plan(G4Phase& ph, int first, int u1, int chunks, const G4Rows* s, const G4Params& p) {
     constexpr int P = G4X<XT>::PARTS, CO = G4X<XT>::COLS;
     const int lane = threadIdx.x & 31;
     if constexpr (!EXPERTS) {
@@ -362,7 +360,7 @@ __device__ __forceinline__ void g4_plan(G4Phase& ph, int first, int u1, const G4
     }
     const int cols = both & 0xFFFF, products = both >> 16;
     // a second product may be read where a slot has only one
-    const bool fits = in && (lane == 0 || (cols <= G4_COLS && (p.c1 - p.c0) * g4_x_bytes(G, products + 1, cols * P) <= p.x_room));
+    const bool fits = in && (lane == 0 || (cols <= G4_COLS && chunks * g4_x_bytes(G, products + 1, cols * P) <= p.x_room));
     const unsigned no = ~__ballot_sync(0xffffffffu, fits);
     const int n = no ? __ffs(no) - 1 : 32;
     if (lane < n) {
@@ -382,66 +380,100 @@ __device__ __forceinline__ void g4_plan(G4Phase& ph, int first, int u1, const G4
     }
 }
 
-// x of the planned columns into shared memory, by all warps.  The loops are kept
-// rolled here and in the kernel's start: this code runs once per launch, from a cold
-// instruction cache, and its size is its cost.
+// x of the planned columns into shared memory, by all warps: first as it is (the
+// next part on its way while one is looked at for its largest value), then in place as
+// the products take it.  The loops are kept rolled here and in the kernel's start: this code
+// runs once per launch, from a cold instruction cache, and its size is its cost.
 template <int XT, int G, bool Z, int WARPS>
-__device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, uint8_t* xs) {
+__device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c0, int chunks, uint8_t* xs) {
     constexpr int P = G4X<XT>::PARTS, XB = G4X<XT>::BYTES;
     const int lane = threadIdx.x & 31, warp = g4_uniform(threadIdx.x >> 5);
-    const int chunks = p.c1 - p.c0, cols = g4_uniform(ph.cols), products = g4_uniform(ph.products);
+    const int cols = g4_uniform(ph.cols), products = g4_uniform(ph.products);
     const int tile = cols * P * 64, x_chunk = g4_x_bytes(G, products, cols * P);
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-        int col = 0, c = warp;
-        while (true) {
-            while (c >= chunks) {
-                c -= chunks;
-                ++col;
-            }
-            if (col >= cols) break;
-            const int k = (p.c0 + c) * G4_CHUNK + 4 * lane;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            if (k < p.K) g4_load_x<XT>((const uint8_t*)p.x + ((long long)ph.row[col] * p.K + k) * XB, v);
-            if (pass == 0) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-                m = __reduce_max_sync(0xffffffffu, m);
-                if (lane == 0 && m) atomicMax(&ph.top[col], m);
+    // the lane's 4 values of chunk c of a column: k = 32 (lane / 8) + 4 (lane % 8)
+    uint8_t* const mine = xs + (lane >> 3) * tile + (lane & 7) * 8;
+    auto load = [&](int col, int c) {
+        uint4 v = {0u, 0u, 0u, 0u};
+        const int k = (c0 + c) * G4_CHUNK + 4 * lane;
+        if (col < cols && k < p.K) {
+            const uint8_t* src = (const uint8_t*)p.x + ((long long)ph.row[col] * p.K + k) * XB;
+            if constexpr (XT == 1) {
+                v = __ldg(reinterpret_cast<const uint4*>(src));
             } else {
-                const uint32_t top = ph.top[col];
-                // the largest lands in [2^13, 2^14); at most 2^126, which still keeps the smallest columns whole
-                const int E = min(126, 13 + 127 - (int)(top >> 23));
-                const float up = __uint_as_float((uint32_t)(127 + E) << 23);
-                if (c == 0 && lane == 0)
-                    ph.down[col] = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : (uint32_t)(127 - E) << 23);
-                // k = 32 (lane / 8) + 4 (lane % 8): columns 8t + 0, 1 (times 1) and 8t + 2, 3 (by 16), or + 4, 5 and + 6, 7
-                v[0] *= up; v[1] *= up;
-                v[2] *= up * 0.0625f; v[3] *= up * 0.0625f;
-                uint8_t* at = xs + c * x_chunk;
-                uint8_t* bytes = at + (lane >> 3) * tile + col * (P * 64) + (lane & 7) * 8;
-                float* sums = reinterpret_cast<float*>(at + 4 * tile) + lane / (G / 4) * products * 8 + ph.sum[col];
-#pragma unroll 1
-                for (int q = 0; q < P; ++q) {
-                    const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
-                    uint2 o;
-                    memcpy(&o.x, &a, 4);
-                    memcpy(&o.y, &b, 4);
-                    *reinterpret_cast<uint2*>(bytes + q * 64) = o;
-                    const float2 f = __half22float2(a), h = __half22float2(b);
-                    v[0] = (v[0] - f.x) * 2048.f; v[1] = (v[1] - f.y) * 2048.f;
-                    v[2] = (v[2] - h.x) * 2048.f; v[3] = (v[3] - h.y) * 2048.f;
-                    float s = fmaf(h.x + h.y, 16.f, f.x + f.y);
-#pragma unroll
-                    for (int d = 1; d < G / 4; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-                    if (lane % (G / 4) == 0) sums[q] = s * (Z ? -0x1.0p-21f : -0x1.0p-18f);
-                }
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+                v.x = u.x;
+                v.y = u.y;
             }
-            c += WARPS;
         }
-        __syncthreads();
+        return v;
+    };
+    auto next = [&](int& col, int& c) {
+        c += WARPS;
+        while (c >= chunks) {
+            c -= chunks;
+            ++col;
+        }
+    };
+    int col = 0, c = warp - WARPS;
+    next(col, c);
+    const int col1 = col, c1 = c;
+    uint4 v = load(col, c);
+#pragma unroll 1
+    while (col < cols) {
+        const int here = col, at = c;
+        next(col, c);
+        const uint4 u = load(col, c);
+        float f[4];
+        g4_x_values<XT>(v, f);
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0 && m) atomicMax(&ph.top[here], m);
+        uint8_t* bytes = mine + at * x_chunk + here * (P * 64);
+        *reinterpret_cast<uint2*>(bytes) = make_uint2(v.x, v.y);
+        if constexpr (XT == 1) *reinterpret_cast<uint2*>(bytes + 64) = make_uint2(v.z, v.w);
+        v = u;
     }
+    __syncthreads();
+    col = col1;
+    c = c1;
+#pragma unroll 1
+    while (col < cols) {
+        uint8_t* bytes = mine + c * x_chunk + col * (P * 64);
+        const uint2 lo = *reinterpret_cast<const uint2*>(bytes);
+        uint2 hi = {0u, 0u};
+        if constexpr (XT == 1) hi = *reinterpret_cast<const uint2*>(bytes + 64);
+        float f[4];
+        g4_x_values<XT>(make_uint4(lo.x, lo.y, hi.x, hi.y), f);
+        const uint32_t top = ph.top[col];
+        // the largest lands in [2^13, 2^14); at most 2^126, which still keeps the smallest columns whole
+        const int E = min(126, 13 + 127 - (int)(top >> 23));
+        const float up = __uint_as_float((uint32_t)(127 + E) << 23);
+        if (c == 0 && lane == 0)
+            ph.down[col] = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : (uint32_t)(127 - E) << 23);
+        // columns 8t + 0, 1 (times 1) and 8t + 2, 3 (by 16), or + 4, 5 and + 6, 7
+        f[0] *= up; f[1] *= up;
+        f[2] *= up * 0.0625f; f[3] *= up * 0.0625f;
+        float* sums = reinterpret_cast<float*>(xs + c * x_chunk + 4 * tile) + lane / (G / 4) * products * 8 + ph.sum[col];
+#pragma unroll 1
+        for (int q = 0; q < P; ++q) {
+            const __half2 a = __floats2half2_rn(f[0], f[1]), b = __floats2half2_rn(f[2], f[3]);
+            uint2 o;
+            memcpy(&o.x, &a, 4);
+            memcpy(&o.y, &b, 4);
+            *reinterpret_cast<uint2*>(bytes + q * 64) = o;
+            const float2 g = __half22float2(a), h = __half22float2(b);
+            f[0] = (f[0] - g.x) * 2048.f; f[1] = (f[1] - g.y) * 2048.f;
+            f[2] = (f[2] - h.x) * 2048.f; f[3] = (f[3] - h.y) * 2048.f;
+            float s = fmaf(h.x + h.y, 16.f, g.x + g.y);
+#pragma unroll
+            for (int d = 1; d < G / 4; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            if (lane % (G / 4) == 0) sums[q] = s * (Z ? -0x1.0p-21f : -0x1.0p-18f);
+        }
+        next(col, c);
+    }
+    __syncthreads();
 }
 
 // A unit is two row-groups against up to p.cols rows of x: rows 32u .. 32u + 31
@@ -465,6 +497,7 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int2 wait_all[WARPS][8];   // (unit, row of y) of the blocks of 32 sums that wait
     __shared__ G4Phase ph;
+    __shared__ float parts[EXPERTS ? 1 : G4_SPLIT][8][32];   // of a cluster's CTAs, in its first one
     // shared memory: sums, rings, x, rows by expert
     float* const red_all = reinterpret_cast<float*>(smem);
     uint8_t* const xs = smem + WARPS * 1024 + WARPS * RING;
@@ -472,18 +505,23 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
     const int lane = threadIdx.x & 31, warp = g4_uniform(threadIdx.x >> 5);
     const int team = warp * p.inv_team >> 16, member = warp - team * p.team, teams = p.teams;
     float* const red = red_all + team * p.team * 256;
-    const int chunks = p.c1 - p.c0;
+    // one matrix of few rows: the p.split CTAs of a cluster share a unit, each a part of K
+    const int split = EXPERTS ? 1 : p.split, rank = EXPERTS ? 0 : blockIdx.x & (split - 1);
+    const int c0 = EXPERTS ? p.c0 : p.c0 + (p.c1 - p.c0) * rank / split;
+    const int chunks = EXPERTS ? p.c1 - p.c0 : p.c0 + (p.c1 - p.c0) * (rank + 1) / split - c0;
+    if (!EXPERTS && split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this CTA is there
     grid_dep_launch();
     grid_dep_wait();
     const int slots = EXPERTS ? g4_uniform(g4_rows<WARPS>(*rows, p)) : 1;
     // the CTA's units u0 .. u1 - 1
-    const int total = slots * p.units, b = blockIdx.x, each = total / gridDim.x, more = total - each * gridDim.x;
+    const int groups = EXPERTS ? gridDim.x : gridDim.x / split;
+    const int total = slots * p.units, b = EXPERTS ? blockIdx.x : blockIdx.x / split, each = total / groups, more = total - each * groups;
     const int u0 = each * b + min(b, more), u1 = u0 + each + (b < more);
     if (u0 == u1) return;
 
     // loads: the next chunk of this warp, in order
     if constexpr (!EXPERTS) {   // the warp's first part of x, on its way while the rest is set up
-        const int k = (p.c0 + warp) * G4_CHUNK + 4 * lane;
+        const int k = (c0 + warp) * G4_CHUNK + 4 * lane;
         if (k < p.K) asm volatile("prefetch.global.L1 [%0];" ::"l"((const uint8_t*)p.x + (long long)k * XB));
     }
     Walk w;
@@ -497,15 +535,15 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
     const int o_tail = (lane >> 4) * (FULL - 256) + 1024;              // the lane's piece behind the codes of either row-group
     const bool has_tail = (lane & 15) * 16 < FULL - 1024;
     // the warp's chunks of a unit; the last of them may be the short end of K
-    const int n = p.each + (member < p.more);
-    const int last = p.K - (p.c0 + member + (n - 1) * p.team) * G4_CHUNK;
+    const int n = (chunks - member + p.team - 1) * p.inv_team >> 16;
+    const int last = p.K - (c0 + member + (n - 1) * p.team) * G4_CHUNK;
     const int end = last < G4_CHUNK ? 1 : 0;                           // chunks to go when the short one is next, 0: there is none
     const int jump = p.team * FULL;
     int fu = u0 + team, fl = fu < u1 ? n : 0, fstage = 0;               // unit and chunks of it still to load, 0: nothing left
     const uint8_t *f0 = nullptr, *f1 = nullptr, *f2 = nullptr;         // the lane's pieces: codes of both, and behind
     Walk f = w;
     auto aim = [&]() {
-        const long long at = f.e * p.stride + (long long)(p.c0 + member) * FULL;
+        const long long at = f.e * p.stride + (long long)(c0 + member) * FULL;
         const uint8_t *r0, *r1;
         if constexpr (PAIR) {
             r0 = p.W0 + at + f.unit * p.rg_bytes;
@@ -569,7 +607,11 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
                 a = g4_silu_mul(a, b);
                 if (lane >= 16) row = p.N;
             }
-            if (row < p.N) {
+            if (!EXPERTS && split > 1) {   // to the cluster's first CTA
+                uint32_t to = smem_u32(&parts[rank][i][lane]);
+                asm volatile("mapa.shared::cluster.u32 %0, %0, 0;" : "+r"(to));
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(a) : "memory");
+            } else if (row < p.N) {
                 float* out = p.y + (long long)q.y * p.N + row;
                 *out = p.c0 ? *out + a : a;
             }
@@ -623,16 +665,17 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
                     }
             }
     };
+    if (!EXPERTS && split > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");      // all are there
     for (int u = u0 + team;;) {
         // x of the next slots, when the CTA is through with the last ones
         first = phase_end < 0 ? first_slot : phase_end;
-        if (warp == 0) g4_plan<XT, G, EXPERTS>(ph, first, u1, rows, p);
+        if (warp == 0) g4_plan<XT, G, EXPERTS>(ph, first, u1, chunks, rows, p);
         __syncthreads();
         phase_end = g4_uniform(ph.end);
         products = g4_uniform(ph.products);
         tile = g4_uniform(ph.cols) * P * 64;
         x_chunk = g4_x_bytes(G, products, g4_uniform(ph.cols) * P);
-        g4_stage_x<XT, G, Z, WARPS>(p, ph, xs);
+        g4_stage_x<XT, G, Z, WARPS>(p, ph, c0, chunks, xs);
         const bool done = !EXPERTS || phase_end * (long long)p.units >= u1;   // the CTA's last slots
 #pragma unroll 1
         while (true) {
@@ -655,6 +698,18 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
         }
         if (done) break;
         __syncthreads();   // x is written again
+    }
+    if (!EXPERTS && split > 1) {
+        // the parts of K, added in the order of the CTAs
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        const int row = 32 * u0 + lane;
+        if (rank == 0 && warp < p.R && row < p.N) {
+            float a = 0.f;
+            for (int r = 0; r < split; ++r) a += parts[r][warp][lane];
+            float* out = p.y + (long long)warp * p.N + row;
+            *out = p.c0 ? *out + a : a;
+        }
     }
 }
 
@@ -686,7 +741,7 @@ cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
     constexpr int P = G4X<XT>::PARTS, CO = G4X<XT>::COLS, WARPS = g4_warps(NBMAX);
     constexpr int FULL = g4_chunk_bytes(G4_CHUNK, G, Z);
     const int fixed = WARPS * 1024 + WARPS * 2 * G4_NR * FULL + (EXPERTS ? (int)sizeof(G4Rows) : 0);
-    const int room = (G4_SMEM - (int)sizeof(G4Phase) - WARPS * 64 - 512 - fixed) & ~127;   // less the kernel's static part
+    const int room = (G4_SMEM - (int)sizeof(G4Phase) - WARPS * 64 - (EXPERTS ? 0 : G4_SPLIT * 1024) - 640 - fixed) & ~127;   // less the kernel's static part
     p.rg_bytes = g4_rowgroup_bytes(p.K, G, Z);
     p.units = PAIR ? (p.N + 15) / 16 : (p.N + 31) / 32;
     const int chunks = (p.K + G4_CHUNK - 1) / G4_CHUNK;
@@ -697,20 +752,25 @@ cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
     int span = 0, x_chunk = 0;
     for (p.shift = 0; EXPERTS && (1 << p.shift) < std::min(p.R, NBMAX * CO); ++p.shift) {}
     p.cols = EXPERTS ? 1 << p.shift : std::min(p.R, NBMAX * CO);
+    // One matrix of few rows: clusters of up to G4_SPLIT CTAs share a unit, as long as a warp has more than one
+    // chunk and all clusters run at once (one CTA a unit / clusters: 500 x 14336, q = 4: 32 / 13 us; 1024 x 7168, q = 2:
+    // 10.9 / 6.3; 200 x 8192, fp32 x, q = 2: 16.6 / 7.0; 4096 x 4096 has a unit for nearly every SM).
+    p.split = 1;
+    while (!EXPERTS && p.split < G4_SPLIT && p.units * 2LL * p.split <= sms && chunks > p.split * WARPS) p.split *= 2;
     while (true) {
         x_chunk = g4_x_bytes(G, (p.cols + CO - 1) / CO + 1, p.cols * P);
-        span = std::min(chunks, room / x_chunk);
+        span = (int)std::min<long long>(chunks, (long long)p.split * (room / x_chunk));
         if (span == chunks || !PAIR || p.cols == 1) break;
         p.cols = 1 << --p.shift;
     }
     if (span < 1 || (PAIR && span < chunks)) return cudaErrorNotSupported;
     // one matrix has one slot; experts up to one per row, and room for several
-    p.x_room = EXPERTS ? room : span * x_chunk;
-    p.team = g4_team((long long)p.units * (EXPERTS ? std::min(p.E, p.R) : 1), span, sms, WARPS);
+    p.x_room = EXPERTS ? room : (span + p.split - 1) / p.split * x_chunk;
+    p.team = p.split > 1 ? WARPS : g4_team((long long)p.units * (EXPERTS ? std::min(p.E, p.R) : 1), span, sms, WARPS);
     p.teams = WARPS / p.team;
     p.inv_team = (65536 + p.team - 1) / p.team;   // warp / team = warp * inv_team >> 16 for fewer than 32 warps
     const long long total = (long long)p.units * (EXPERTS ? p.R : 1);
-    const int grid = (int)std::min<long long>(sms, total);
+    const int grid = p.split > 1 ? p.units * p.split : (int)std::min<long long>(sms, total);
     const int smem = fixed + p.x_room;
     auto kernel = g4_kernel<XT, G, Z, MODE, NBMAX>;
     static SmemLimit limit;   // one per instantiation
@@ -724,9 +784,8 @@ cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
         }
         for (p.c0 = 0; p.c0 < chunks && e == cudaSuccess; p.c0 = p.c1) {
             p.c1 = std::min(chunks, p.c0 + span);
-            p.each = (p.c1 - p.c0) / p.team;
-            p.more = (p.c1 - p.c0) % p.team;
-            e = launch_dependent(kernel, grid, WARPS * 32, smem, stream, p);
+            e = p.split > 1 ? launch_clusters(kernel, grid, p.split, WARPS * 32, smem, stream, p)
+                            : launch_dependent(kernel, grid, WARPS * 32, smem, stream, p);
         }
     }
     return e;

@@ -66,4 +66,25 @@ cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The same in clusters of `cluster` CTAs.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(Params...), unsigned grid, unsigned cluster, unsigned block, size_t smem,
+                            cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    (void)cudaGetLastError();   // an earlier call's launch error is not this launch's
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace rfx

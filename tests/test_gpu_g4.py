@@ -71,7 +71,7 @@ def check(y, W, x, G, integer=False):
 
 
 SHAPES = [(1, 32, 32), (16, 64, 64), (17, 288, 32), (33, 128, 128), (100, 320, 64), (64, 4096, 128), (250, 2048, 32),
-          (4096, 256, 64), (5000, 96, 32), (48, 14336, 128), (31, 7168, 64), (20000, 512, 128)]
+          (4096, 256, 64), (5000, 96, 32), (48, 14336, 128), (31, 7168, 64), (20000, 512, 128), (70, 12320, 32), (2300, 3200, 64)]
 
 
 @pytest.mark.parametrize("zeros", [False, True])
