@@ -225,7 +225,7 @@ int moe_group_tokens(const void* x, rfx_dtype dtype, int T, int H, const int32_t
  * Gradient of moe_group_tokens with respect to x: dx[t] = sum_j dxs[pos[t][j]],
  * j ascending, summed in fp32 and rounded once to dtype.  An entry of pos
  * outside [0, T * k) contributes nothing.  dxs: device [T * k][H]; dx: device
- * [T][H], both of dtype.
+ * [T][H], both of dtype; they may not overlap.
  */
 int moe_group_tokens_backward(const void* dxs, rfx_dtype dtype, int T, int H, const int32_t* pos, int k, void* dx,
                               void* stream);

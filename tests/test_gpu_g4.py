@@ -270,6 +270,23 @@ def test_expert_products_of_many_passes(K, dtype, rows):
     assert bool(((h.double() - want).abs() <= bound).all())
 
 
+def test_experts_past_4_gib_and_no_rows():
+    N, K, G = 48, 256, 64
+    w = G4(N, K, G, True, 7, E=3, integer=True)
+    stride = (5 << 30) // 2                            # the third matrix begins at 5 GiB
+    far = torch.empty(2 * stride + w.stride, dtype=torch.uint8, device=DEV)
+    for e in range(3):
+        far[e * stride:e * stride + w.stride] = w.packed[e * w.stride:(e + 1) * w.stride]
+    counts = [2, 1, 3]
+    x = x_of((6, K), BF, 3, True)
+    y = torch.empty((6, N), device=DEV)
+    rfx.moe_gemv_g4(far, stride, N, K, G, x, offsets_of(counts), y, zeros=True)
+    for e, lo in ((0, 0), (1, 2), (2, 3)):
+        check(y[lo:lo + counts[e]], w.dense(e), x[lo:lo + counts[e]], G, integer=True)
+    none = torch.empty((0, K), dtype=BF, device=DEV)
+    rfx.moe_gemv_g4(far, stride, N, K, G, none, offsets_of([0, 0, 0]), torch.empty((0, N), device=DEV), zeros=True)
+
+
 def test_first_call_inside_a_capture():
     # in a process of its own: nothing of the library has run before the capture
     code = (

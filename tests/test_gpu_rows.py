@@ -83,7 +83,8 @@ def check_group(x, idx_np, E):
 @pytest.mark.parametrize("dtype", [BF, HF, FF])
 @pytest.mark.parametrize("T,H,k,E", [(1, 8, 1, 1), (1, 4096, 6, 256), (4, 4096, 6, 256), (3, 1, 2, 5), (7, 33, 3, 4),
                                      (64, 250, 8, 9), (700, 72, 6, 300), (1500, 64, 8, 1024), (5000, 17, 2, 3),
-                                     (9001, 40, 4, 64), (5, 8, 4, 2), (700, 2056, 6, 3)])
+                                     (9001, 40, 4, 64), (5, 8, 4, 2), (700, 2056, 6, 3), (60000, 16, 8, 256),
+                                     (30000, 9, 16, 1000)])
 def test_group_places_and_rows(T, H, k, E, dtype):
     rng = np.random.default_rng(T * 31 + H)
     x = torch.randn((T, H), device=DEV).to(dtype)
@@ -139,6 +140,47 @@ def test_group_places_only():
     p, r, o = plan_numpy(idx, E)
     assert np.array_equal(pos.cpu().numpy(), p) and np.array_equal(off.cpu().numpy(), o)
     assert np.array_equal(rows.cpu().numpy()[:o[-1]], r)
+
+
+def test_rows_past_4_gib():
+    T, H, k, E = 70000, 4096, 8, 64                 # 4.6 GB of grouped rows
+    rng = np.random.default_rng(12)
+    idx_np = make_idx(rng, T, k, E, "uniform")
+    x = torch.randn((T, H), device=DEV).to(BF)
+    xs, pos, rows, off, ws = group(x, torch.from_numpy(idx_np).to(DEV), E)
+    p, r, o = plan_numpy(idx_np, E)
+    assert np.array_equal(pos.cpu().numpy(), p) and np.array_equal(off.cpu().numpy(), o)
+    some = torch.from_numpy(np.unique(np.concatenate([rng.integers(0, T * k, 500), [0, T * k - 1]]))).to(DEV)
+    assert torch.equal(xs[some], x[rows[some].long() // k])
+    w = torch.rand((T, k), device=DEV)
+    y = torch.empty((T, H), dtype=BF, device=DEV)
+    rfx.moe_combine_rows(xs, pos, w, y)
+    t = torch.from_numpy(np.concatenate([rng.integers(0, T, 50), [T - 1]])).to(DEV)
+    # every row of a token is the token itself: y = (sum_j w_j) x
+    check_sum(y[t], w[t].double().sum(1, keepdim=True) * x[t].double(),
+              w[t].double().sum(1, keepdim=True) * x[t].double().abs(), terms=k + 1)
+    dw = torch.empty_like(w)
+    rfx.moe_combine_rows_backward(x, xs, pos, w, xs, dw)      # gradients over the rows themselves
+    sq = (x[t].double() ** 2).sum(1, keepdim=True)
+    assert bool(((dw[t].double() - sq).abs() <= H * U * sq).all())
+    got = xs[pos[t].long()].double()
+    want = w[t].double()[..., None] * x[t].double()[:, None, :]
+    assert bool(((got - want).abs() <= (half_step(BF) + U) * (1 + half_step(BF)) * want.abs()).all())
+
+
+def test_no_tokens_is_a_no_op():
+    i = torch.empty((0, 4), dtype=torch.int32, device=DEV)
+    f = torch.empty((0, 4), device=DEV)
+    x = torch.empty((0, 16), device=DEV)
+    off = torch.full((9,), 3, dtype=torch.int32, device=DEV)
+    flat = torch.empty(0, dtype=torch.int32, device=DEV)
+    rfx.moe_group_tokens(x, i, 8, x.clone(), i, flat, off, torch.empty(0, dtype=torch.uint8, device=DEV))
+    rfx.moe_combine_rows(x, i, f, x.clone())
+    rfx.moe_combine_rows_backward(x, x, i, f, x.clone(), f)
+    rfx.moe_group_tokens_backward(x, i, x.clone())
+    rfx.moe_router_topk_backward(i, f, f, torch.empty((0, 8), device=DEV))
+    torch.cuda.synchronize()
+    assert (off == 3).all()
 
 
 # ------------------------------------------------------------- combine ---
