@@ -82,21 +82,28 @@ __device__ __forceinline__ void g4_mma(float d[4], const uint32_t a[4], uint32_t
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// Four x values as they lie in memory, as fp32.
+// Eight x values as they lie in memory, and as fp32.
+template <int XT> struct G4Raw { uint4 v[XT == 1 ? 2 : 1]; };
+
 template <int XT>
-__device__ __forceinline__ void g4_x_values(uint4 q, float v[4]) {
+__device__ __forceinline__ void g4_x_values(const G4Raw<XT>& r, float f[8]) {
     if constexpr (XT == 1) {
-        v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
-        v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
-    } else if constexpr (XT == 0) {
-        v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xFFFF0000u);
-        v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xFFFF0000u);
+        memcpy(f, r.v, 32);
     } else {
-        __half2 a, b;
-        memcpy(&a, &q.x, 4);
-        memcpy(&b, &q.y, 4);
-        const float2 f = __half22float2(a), h = __half22float2(b);
-        v[0] = f.x; v[1] = f.y; v[2] = h.x; v[3] = h.y;
+        const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (XT == 0) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            } else {
+                __half2 h;
+                memcpy(&h, &w[i], 4);
+                const float2 g = __half22float2(h);
+                f[2 * i] = g.x;
+                f[2 * i + 1] = g.y;
+            }
+        }
     }
 }
 
@@ -380,98 +387,106 @@ __device__ __forceinline__ void g4_plan(G4Phase& ph, int first, int u1, int chun
     }
 }
 
-// x of the planned columns into shared memory, by all warps: first as it is (the
-// next part on its way while one is looked at for its largest value), then in place as
-// the products take it.  The loops are kept rolled here and in the kernel's start: this code
-// runs once per launch, from a cold instruction cache, and its size is its cost.
+// x of the planned columns into shared memory, by all warps: first as it is (the next part on its way
+// while one is looked at for its largest value), then in place as the products take it.
+// A warp takes two chunks of a column at a time, a lane 8 values.  Each turn is a chain of dependent
+// steps (about 1100 cycles to the first values from memory, then several hundred a turn), so few wide turns win:
+// 4096 x 4096, q = 8, 11.1 us against 14.2 with one chunk and 4 values a lane; q = 1, 6.7 against 7.0.
 template <int XT, int G, bool Z, int WARPS>
 __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c0, int chunks, uint8_t* xs) {
     constexpr int P = G4X<XT>::PARTS, XB = G4X<XT>::BYTES;
-    const int lane = threadIdx.x & 31, warp = g4_uniform(threadIdx.x >> 5);
-    const int cols = g4_uniform(ph.cols), products = g4_uniform(ph.products);
+    const int lane = threadIdx.x & 31, warp = g4_uniform(threadIdx.x >> 5), l = lane & 15;
+    const int cols = g4_uniform(ph.cols), products = g4_uniform(ph.products), pairs = (chunks + 1) >> 1;
     const int tile = cols * P * 64, x_chunk = g4_x_bytes(G, products, cols * P);
-    // the lane's 4 values of chunk c of a column: k = 32 (lane / 8) + 4 (lane % 8)
-    uint8_t* const mine = xs + (lane >> 3) * tile + (lane & 7) * 8;
-    auto load = [&](int col, int c) {
-        uint4 v = {0u, 0u, 0u, 0u};
-        const int k = (c0 + c) * G4_CHUNK + 4 * lane;
-        if (col < cols && k < p.K) {
-            const uint8_t* src = (const uint8_t*)p.x + ((long long)ph.row[col] * p.K + k) * XB;
-            if constexpr (XT == 1) {
-                v = __ldg(reinterpret_cast<const uint4*>(src));
-            } else {
-                const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
-                v.x = u.x;
-                v.y = u.y;
-            }
+    // the lane's values of chunk 2i + lane / 16: columns 8l .. 8l + 7
+    uint8_t* const mine = xs + (lane >> 4) * x_chunk + (l >> 2) * tile + (l & 3) * 16;
+    const int k0 = (c0 + (lane >> 4)) * G4_CHUNK + 8 * l;
+    auto load = [&](int col, int i) {
+        G4Raw<XT> r = {};
+        const int k = k0 + i * (2 * G4_CHUNK);
+        if (col < cols && 2 * i + (lane >> 4) < chunks && k < p.K) {
+            const uint4* src = reinterpret_cast<const uint4*>((const uint8_t*)p.x + ((long long)ph.row[col] * p.K + k) * XB);
+            r.v[0] = __ldg(src);
+            if constexpr (XT == 1) r.v[1] = __ldg(src + 1);
         }
-        return v;
+        return r;
     };
-    auto next = [&](int& col, int& c) {
-        c += WARPS;
-        while (c >= chunks) {
-            c -= chunks;
+    auto next = [&](int& col, int& i) {
+        i += WARPS;
+        while (i >= pairs) {
+            i -= pairs;
             ++col;
         }
     };
-    int col = 0, c = warp - WARPS;
-    next(col, c);
-    const int col1 = col, c1 = c;
-    uint4 v = load(col, c);
+    int col = 0, i = warp - WARPS;
+    next(col, i);
+    const int col1 = col, i1 = i;
+    G4Raw<XT> v = load(col, i);
 #pragma unroll 1
     while (col < cols) {
-        const int here = col, at = c;
-        next(col, c);
-        const uint4 u = load(col, c);
-        float f[4];
+        const int here = col, at = i;
+        next(col, i);
+        const G4Raw<XT> u = load(col, i);
+        float f[8];
         g4_x_values<XT>(v, f);
         uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0 && m) atomicMax(&ph.top[here], m);
-        uint8_t* bytes = mine + at * x_chunk + here * (P * 64);
-        *reinterpret_cast<uint2*>(bytes) = make_uint2(v.x, v.y);
-        if constexpr (XT == 1) *reinterpret_cast<uint2*>(bytes + 64) = make_uint2(v.z, v.w);
+        if (2 * at + (lane >> 4) < chunks) {
+            uint8_t* bytes = mine + 2 * at * x_chunk + here * (P * 64);
+            *reinterpret_cast<uint4*>(bytes) = v.v[0];
+            if constexpr (XT == 1) *reinterpret_cast<uint4*>(bytes + 64) = v.v[1];
+        }
         v = u;
     }
     __syncthreads();
     col = col1;
-    c = c1;
+    i = i1;
 #pragma unroll 1
     while (col < cols) {
-        uint8_t* bytes = mine + c * x_chunk + col * (P * 64);
-        const uint2 lo = *reinterpret_cast<const uint2*>(bytes);
-        uint2 hi = {0u, 0u};
-        if constexpr (XT == 1) hi = *reinterpret_cast<const uint2*>(bytes + 64);
-        float f[4];
-        g4_x_values<XT>(make_uint4(lo.x, lo.y, hi.x, hi.y), f);
+        const bool in = 2 * i + (lane >> 4) < chunks;
+        uint8_t* bytes = mine + 2 * i * x_chunk + col * (P * 64);
+        G4Raw<XT> r = {};
+        if (in) {
+            r.v[0] = *reinterpret_cast<const uint4*>(bytes);
+            if constexpr (XT == 1) r.v[1] = *reinterpret_cast<const uint4*>(bytes + 64);
+        }
+        float f[8];
+        g4_x_values<XT>(r, f);
         const uint32_t top = ph.top[col];
         // the largest lands in [2^13, 2^14); at most 2^126, which still keeps the smallest columns whole
         const int E = min(126, 13 + 127 - (int)(top >> 23));
         const float up = __uint_as_float((uint32_t)(127 + E) << 23);
-        if (c == 0 && lane == 0)
+        if (i == 0 && lane == 0)
             ph.down[col] = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : (uint32_t)(127 - E) << 23);
-        // columns 8t + 0, 1 (times 1) and 8t + 2, 3 (by 16), or + 4, 5 and + 6, 7
-        f[0] *= up; f[1] *= up;
-        f[2] *= up * 0.0625f; f[3] *= up * 0.0625f;
-        float* sums = reinterpret_cast<float*>(xs + c * x_chunk + 4 * tile) + lane / (G / 4) * products * 8 + ph.sum[col];
+        // columns 0, 1, 4, 5 times 1, columns 2, 3, 6, 7 by 16
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] *= j & 2 ? up * 0.0625f : up;
+        float* sums = reinterpret_cast<float*>(xs + (2 * i + (lane >> 4)) * x_chunk + 4 * tile) + l / (G / 8) * products * 8 + ph.sum[col];
 #pragma unroll 1
         for (int q = 0; q < P; ++q) {
-            const __half2 a = __floats2half2_rn(f[0], f[1]), b = __floats2half2_rn(f[2], f[3]);
-            uint2 o;
-            memcpy(&o.x, &a, 4);
-            memcpy(&o.y, &b, 4);
-            *reinterpret_cast<uint2*>(bytes + q * 64) = o;
-            const float2 g = __half22float2(a), h = __half22float2(b);
-            f[0] = (f[0] - g.x) * 2048.f; f[1] = (f[1] - g.y) * 2048.f;
-            f[2] = (f[2] - h.x) * 2048.f; f[3] = (f[3] - h.y) * 2048.f;
-            float s = fmaf(h.x + h.y, 16.f, g.x + g.y);
+            uint32_t o[4];
+            float s[2] = {0.f, 0.f};   // of the values times 1, and by 16
 #pragma unroll
-            for (int d = 1; d < G / 4; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            if (lane % (G / 4) == 0) sums[q] = s * (Z ? -0x1.0p-21f : -0x1.0p-18f);
+            for (int j = 0; j < 4; ++j) {
+                const __half2 h = __floats2half2_rn(f[2 * j], f[2 * j + 1]);
+                memcpy(&o[j], &h, 4);
+                const float2 g = __half22float2(h);
+                s[j & 1] += g.x + g.y;
+                if constexpr (P > 1) {
+                    f[2 * j] = (f[2 * j] - g.x) * 2048.f;
+                    f[2 * j + 1] = (f[2 * j + 1] - g.y) * 2048.f;
+                }
+            }
+            if (in) *reinterpret_cast<uint4*>(bytes + q * 64) = make_uint4(o[0], o[1], o[2], o[3]);
+            float sum = fmaf(s[1], 16.f, s[0]);
+#pragma unroll
+            for (int d = 1; d < G / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (in && l % (G / 8) == 0) sums[q] = sum * (Z ? -0x1.0p-21f : -0x1.0p-18f);
         }
-        next(col, c);
+        next(col, i);
     }
     __syncthreads();
 }
