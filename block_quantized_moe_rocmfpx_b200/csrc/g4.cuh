@@ -778,7 +778,7 @@ cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
         if (span == chunks || !PAIR || p.cols == 1) break;
         p.cols = 1 << --p.shift;
     }
-    if (span < 1 || (PAIR && span < chunks)) return cudaErrorNotSupported;
+    if (span < 1 || (PAIR && span < chunks) || (span < chunks && span < 2 * p.split)) return cudaErrorNotSupported;
     // one matrix has one slot; experts up to one per row, and room for several
     p.x_room = EXPERTS ? room : (span + p.split - 1) / p.split * x_chunk;
     p.team = p.split > 1 ? WARPS : g4_team((long long)p.units * (EXPERTS ? std::min(p.E, p.R) : 1), span, sms, WARPS);
@@ -799,6 +799,8 @@ cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
         }
         for (p.c0 = 0; p.c0 < chunks && e == cudaSuccess; p.c0 = p.c1) {
             p.c1 = std::min(chunks, p.c0 + span);
+            // every CTA of a cluster has a chunk at least, in the last part too (its span is 2 a CTA or more)
+            if (p.c1 < chunks && chunks - p.c1 < p.split) p.c1 = chunks - p.split;
             e = p.split > 1 ? launch_clusters(kernel, grid, p.split, WARPS * 32, smem, stream, p)
                             : launch_dependent(kernel, grid, WARPS * 32, smem, stream, p);
         }

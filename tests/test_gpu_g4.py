@@ -125,6 +125,20 @@ def test_gemv_columns_are_independent(dtype):
     assert torch.isnan(yb[2]).all() and not torch.isfinite(yb[5]).any()
 
 
+@pytest.mark.parametrize("dtype,q,zeros,chunks", [(BF, 8, False, 352), (HF, 7, True, 344), (FF, 4, False, 344), (FF, 2, True, 456)])
+def test_gemv_of_several_parts_of_K(dtype, q, zeros, chunks):
+    # x of all K does not fit the shared memory of a cluster: the last part may be shorter than the cluster is wide.
+    # |w x| <= 15 * 2 * 4, in units of 1/2: sums below 2^24 up to K = 69,000
+    N, G = 40, 128
+    for n in range(chunks - 12, chunks + 20):
+        K = 128 * n
+        w = G4(N, K, G, zeros, n, integer=True)
+        x = x_of((q, K), dtype, n, True).clamp(-4, 4)
+        y = torch.full((q, N), float("nan"), device=DEV)
+        rfx.rfx_gemv_g4(w.packed, N, K, G, x, y, zeros=zeros)
+        check(y, w.dense(), x, G, integer=True)
+
+
 def test_gemv_fp32_x_of_any_size():
     # 24-bit significands from 2^-60 to 2^60 in one row: the parts lose nothing
     N, K, G = 64, 512, 32
