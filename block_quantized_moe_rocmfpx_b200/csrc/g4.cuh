@@ -387,29 +387,39 @@ __device__ __forceinline__ void g4_plan(G4Phase& ph, int first, int u1, int chun
     }
 }
 
+// The lane's 8 values of chunk c or c + 1 of a row of x (0 behind the last).
+template <int XT>
+__device__ __forceinline__ G4Raw<XT> g4_x_load(const G4Params& p, int row, int c0, int chunks, int c) {
+    const int lane = threadIdx.x & 31;
+    G4Raw<XT> r = {};
+    c += lane >> 4;
+    const int k = (c0 + c) * G4_CHUNK + (lane & 15) * 8;
+    if (c < chunks && k < p.K) {
+        const uint4* src = reinterpret_cast<const uint4*>((const uint8_t*)p.x + ((long long)row * p.K + k) * G4X<XT>::BYTES);
+        r.v[0] = __ldg(src);
+        if constexpr (XT == 1) r.v[1] = __ldg(src + 1);
+    }
+    return r;
+}
+
+// One matrix: a warp's first part of x, asked for before anything else.
+template <int XT> struct G4XFirst { int col, i; G4Raw<XT> v; };
+
 // x of the planned columns into shared memory, by all warps: first as it is (the next part on its way
 // while one is looked at for its largest value), then in place as the products take it.
 // A warp takes two chunks of a column at a time, a lane 8 values.  Each turn is a chain of dependent
 // steps (about 1100 cycles to the first values from memory, then several hundred a turn), so few wide turns win:
 // 4096 x 4096, q = 8, 11.1 us against 14.2 with one chunk and 4 values a lane; q = 1, 6.7 against 7.0.
 template <int XT, int G, bool Z, int WARPS>
-__device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c0, int chunks, uint8_t* xs) {
-    constexpr int P = G4X<XT>::PARTS, XB = G4X<XT>::BYTES;
+__device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c0, int chunks, uint8_t* xs, const G4XFirst<XT>* begun) {
+    constexpr int P = G4X<XT>::PARTS;
     const int lane = threadIdx.x & 31, warp = g4_uniform(threadIdx.x >> 5), l = lane & 15;
     const int cols = g4_uniform(ph.cols), products = g4_uniform(ph.products), pairs = (chunks + 1) >> 1;
     const int tile = cols * P * 64, x_chunk = g4_x_bytes(G, products, cols * P);
     // the lane's values of chunk 2i + lane / 16: columns 8l .. 8l + 7
     uint8_t* const mine = xs + (lane >> 4) * x_chunk + (l >> 2) * tile + (l & 3) * 16;
-    const int k0 = (c0 + (lane >> 4)) * G4_CHUNK + 8 * l;
     auto load = [&](int col, int i) {
-        G4Raw<XT> r = {};
-        const int k = k0 + i * (2 * G4_CHUNK);
-        if (col < cols && 2 * i + (lane >> 4) < chunks && k < p.K) {
-            const uint4* src = reinterpret_cast<const uint4*>((const uint8_t*)p.x + ((long long)ph.row[col] * p.K + k) * XB);
-            r.v[0] = __ldg(src);
-            if constexpr (XT == 1) r.v[1] = __ldg(src + 1);
-        }
-        return r;
+        return col < cols ? g4_x_load<XT>(p, ph.row[col], c0, chunks, 2 * i) : G4Raw<XT>();
     };
     auto next = [&](int& col, int& i) {
         i += WARPS;
@@ -419,9 +429,16 @@ __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c
         }
     };
     int col = 0, i = warp - WARPS;
-    next(col, i);
+    G4Raw<XT> v;
+    if (begun) {
+        col = begun->col;
+        i = begun->i;
+        v = begun->v;
+    } else {
+        next(col, i);
+        v = load(col, i);
+    }
     const int col1 = col, i1 = i;
-    G4Raw<XT> v = load(col, i);
 #pragma unroll 1
     while (col < cols) {
         const int here = col, at = i;
@@ -505,7 +522,7 @@ __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c
 template <int XT, int G, bool Z, int MODE, int NBMAX>
 __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p) {
     constexpr int FULL = g4_chunk_bytes(G4_CHUNK, G, Z);
-    constexpr int P = G4X<XT>::PARTS, XB = G4X<XT>::BYTES, WARPS = g4_warps(NBMAX);
+    constexpr int P = G4X<XT>::PARTS, WARPS = g4_warps(NBMAX);
     constexpr bool EXPERTS = MODE > 0, PAIR = MODE == 2;
     using Walk = G4Walk<EXPERTS>;
     constexpr int STAGE = G4_NR * FULL, RING = 2 * STAGE;
@@ -535,9 +552,12 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
     if (u0 == u1) return;
 
     // loads: the next chunk of this warp, in order
+    G4XFirst<XT> begun;
     if constexpr (!EXPERTS) {   // the warp's first part of x, on its way while the rest is set up
-        const int k = (c0 + warp) * G4_CHUNK + 4 * lane;
-        if (k < p.K) asm volatile("prefetch.global.L1 [%0];" ::"l"((const uint8_t*)p.x + (long long)k * XB));
+        const int pairs = (chunks + 1) >> 1;
+        begun.col = warp / pairs;
+        begun.i = warp - begun.col * pairs;
+        begun.v = begun.col < p.R ? g4_x_load<XT>(p, begun.col, c0, chunks, 2 * begun.i) : G4Raw<XT>();
     }
     Walk w;
     const int first_slot = EXPERTS ? u0 / p.units : 0;
@@ -690,7 +710,7 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
         products = g4_uniform(ph.products);
         tile = g4_uniform(ph.cols) * P * 64;
         x_chunk = g4_x_bytes(G, products, g4_uniform(ph.cols) * P);
-        g4_stage_x<XT, G, Z, WARPS>(p, ph, c0, chunks, xs);
+        g4_stage_x<XT, G, Z, WARPS>(p, ph, c0, chunks, xs, EXPERTS ? nullptr : &begun);
         const bool done = !EXPERTS || phase_end * (long long)p.units >= u1;   // the CTA's last slots
 #pragma unroll 1
         while (true) {
