@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
     const int team = warp * p.inv_team >> 16, member = warp - team * p.team, teams = p.teams;
     float* const red = red_all + team * p.team * 256;
     // one matrix of few rows: the p.split CTAs of a cluster share a unit, each a part of K
-    const int split = EXPERTS ? 1 : p.split, rank = EXPERTS ? 0 : blockIdx.x & (split - 1);
+    const int split = EXPERTS ? 1 : p.split, rank = EXPERTS ? 0 : blockIdx.x % split;
     const int c0 = EXPERTS ? p.c0 : p.c0 + (p.c1 - p.c0) * rank / split;
     const int chunks = EXPERTS ? p.c1 - p.c0 : p.c0 + (p.c1 - p.c0) * (rank + 1) / split - c0;
     if (!EXPERTS && split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this CTA is there
@@ -787,11 +787,25 @@ cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
     int span = 0, x_chunk = 0;
     for (p.shift = 0; EXPERTS && (1 << p.shift) < std::min(p.R, NBMAX * CO); ++p.shift) {}
     p.cols = EXPERTS ? 1 << p.shift : std::min(p.R, NBMAX * CO);
-    // One matrix of few rows: clusters of up to G4_SPLIT CTAs share a unit, as long as a warp has more than one
-    // chunk and all clusters run at once (one CTA a unit / clusters: 500 x 14336, q = 4: 32 / 13 us; 1024 x 7168, q = 2:
-    // 10.9 / 6.3; 200 x 8192, fp32 x, q = 2: 16.6 / 7.0; 4096 x 4096 has a unit for nearly every SM).
+    auto kernel = g4_kernel<XT, G, Z, MODE, NBMAX>;
+    static SmemLimit limit;   // one per instantiation
+    static ClusterFit fit;
+    // One matrix of few rows: clusters of up to G4_SPLIT CTAs share a unit, down to 8 chunks a CTA (few
+    // turns of staging x), as long as all clusters run at once; odd sizes leave halves of SM pairs idle and take longer
+    // than the occupancy says when nearly all of theirs are needed.  us, one CTA a unit / clusters of 2 / these:
+    // 500 x 14336, q = 4: 22.5 / - / 6.9 (16 clusters of 8 do not fit: 12.4); 1024 x 4096, q = 8: 9.8 / 7.5 / 6.4; 200 x 8192,
+    // fp32 x, q = 2: 15.8 / - / 5.0; 1400 x 4096, q = 8 (44 units): - / 7.6 / 7.6, of 3: 8.1.
     p.split = 1;
-    while (!EXPERTS && p.split < G4_SPLIT && p.units * 2LL * p.split <= sms && chunks > p.split * WARPS) p.split *= 2;
+    if (!EXPERTS && p.units < sms) {
+        int split = std::min(G4_SPLIT, (chunks + 7) / 8);   // not by the columns: a column's sums do not depend on the others
+        if (split > 1) e = limit.ensure((const void*)kernel, fixed + room);
+        for (int clusters = 0; split > 1 && e == cudaSuccess; --split) {
+            e = fit.get(kernel, split, WARPS * 32, fixed + room, clusters);
+            if (p.units <= (split & 1 ? clusters * 7 / 8 : clusters)) break;
+        }
+        if (e != cudaSuccess) return e;
+        p.split = split;
+    }
     while (true) {
         x_chunk = g4_x_bytes(G, (p.cols + CO - 1) / CO + 1, p.cols * P);
         span = (int)std::min<long long>(chunks, (long long)p.split * (room / x_chunk));
@@ -807,8 +821,6 @@ cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
     const long long total = (long long)p.units * (EXPERTS ? p.R : 1);
     const int grid = p.split > 1 ? p.units * p.split : (int)std::min<long long>(sms, total);
     const int smem = fixed + p.x_room;
-    auto kernel = g4_kernel<XT, G, Z, MODE, NBMAX>;
-    static SmemLimit limit;   // one per instantiation
     e = limit.ensure((const void*)kernel, smem);
     const int all = p.R;
     for (int r = 0; r < all && e == cudaSuccess; r += p.R) {

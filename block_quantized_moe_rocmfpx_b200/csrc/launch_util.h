@@ -46,6 +46,37 @@ inline cudaError_t device_sms(int& sms) {
     return e;
 }
 
+// How many clusters of `size` (at most 8) CTAs of a kernel run on the current device at once, asked once per
+// kernel (an object each), device and size.
+class ClusterFit {
+  public:
+    template <typename... Params>
+    cudaError_t get(void (*kernel)(Params...), int size, unsigned block, size_t smem, int& clusters) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const bool cached = dev >= 0 && dev < kDevices;
+        if (cached && (clusters = fit_[dev][size].load(std::memory_order_relaxed) - 1) >= 0) return cudaSuccess;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(block);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = size;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+        if (e == cudaSuccess && cached) fit_[dev][size].store(clusters + 1, std::memory_order_relaxed);
+        return e;
+    }
+
+  private:
+    static constexpr int kDevices = 64;
+    std::atomic<int> fit_[kDevices][9] = {};
+};
+
 // Launch as a programmatic dependent of the kernel before it on the stream:
 // the launch overlaps that kernel's tail, and the kernel itself waits
 // (grid_dep_wait) before its first access to global memory.

@@ -139,6 +139,19 @@ def test_gemv_of_several_parts_of_K(dtype, q, zeros, chunks):
         check(y, w.dense(), x, G, integer=True)
 
 
+@pytest.mark.parametrize("N,K", [(40, 4096), (500, 14336), (800, 8192), (1400, 4096), (4096, 2048)])
+def test_gemv_columns_are_independent_in_clusters(N, K):
+    w = G4(N, K, 64, False, 6)
+    x = x_of((8, K), BF, 1, False)
+    y8 = torch.empty((8, N), device=DEV)
+    rfx.rfx_gemv_g4(w.packed, N, K, 64, x, y8)
+    check(y8, w.dense(), x, 64)
+    for c in (0, 7):
+        y1 = torch.empty((1, N), device=DEV)
+        rfx.rfx_gemv_g4(w.packed, N, K, 64, x[c:c + 1].contiguous(), y1)
+        assert torch.equal(y1[0], y8[c])
+
+
 def test_gemv_fp32_x_of_any_size():
     # 24-bit significands from 2^-60 to 2^60 in one row: the parts lose nothing
     N, K, G = 64, 512, 32
@@ -318,6 +331,23 @@ def test_first_call_inside_a_capture():
         "g.replay()\n"
         "torch.cuda.synchronize()\n"
         "assert (y == 0).all() and (z == 0).all()\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_first_clusters_inside_a_capture():
+    code = (
+        "import torch, block_quantized_moe_rocmfpx_b200 as rfx\n"
+        "d = 'cuda'\n"
+        "W = torch.zeros(rfx.rfx_g4_packed_bytes(64, 4096, 64), dtype=torch.uint8, device=d)\n"
+        "x, y = torch.ones((2, 4096), device=d).bfloat16(), torch.ones((2, 64), device=d)\n"
+        "g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    rfx.rfx_gemv_g4(W, 64, 4096, 64, x, y)\n"
+        "y.fill_(5)\n"
+        "g.replay()\n"
+        "torch.cuda.synchronize()\n"
+        "assert (y == 0).all()\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
 
