@@ -242,7 +242,15 @@ struct G4Rows {
     int32_t blk[G4_MAXE + 1];
     int32_t lo[G4_MAXE], hi[G4_MAXE];
     int32_t wsum[32];
+    int32_t first, near[32];   // the CTA's first slot; the experts of it and the next
 };
+
+// The CTA's units u0 .. u1 - 1 of all of `slots` slots.
+__device__ __forceinline__ void g4_share(int slots, int groups, int b, const G4Params& p, int& u0, int& u1) {
+    const int total = slots * p.units, each = total / groups, more = total - each * groups;
+    u0 = each * b + min(b, more);
+    u1 = u0 + each + (b < more);
+}
 
 template <int WARPS>
 __device__ __forceinline__ int g4_rows(G4Rows& s, const G4Params& p) {
@@ -276,12 +284,20 @@ __device__ __forceinline__ int g4_rows(G4Rows& s, const G4Params& p) {
     const int sums = scan(lane < WARPS ? s.wsum[lane] : 0);
     int at = sum - own + (warp ? __shfl_sync(0xffffffffu, sums, warp - 1) : 0);
     const int all = __shfl_sync(0xffffffffu, sums, 31);
+    int u0, u1;
+    g4_share(all, gridDim.x, blockIdx.x, p, u0, u1);
+    const int first = u0 / p.units;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         if (PER * tid + i <= p.E) s.blk[PER * tid + i] = at;
+#pragma unroll 1
+        for (int slot = max(at, first); slot < min(at + n[i], first + 32); ++slot) s.near[slot - first] = PER * tid + i;
         at += n[i];
     }
-    if (tid == 0) s.blk[p.E] = all;
+    if (tid == 0) {
+        s.blk[p.E] = all;
+        s.first = first;
+    }
     __syncthreads();
     return all;
 }
@@ -293,6 +309,7 @@ struct G4Walk {
     int slot, unit, e;
     static __device__ __forceinline__ int find(int slot, const G4Rows* s, const G4Params& p) {
         if constexpr (!EXPERTS) return 0;
+        if ((unsigned)(slot - s->first) < 32) return s->near[slot - s->first];
         int e = 0;          // the largest e with blk[e] <= slot
 #pragma unroll 1
         for (int hi = p.E; hi - e > 1;) {
@@ -387,6 +404,23 @@ __device__ __forceinline__ void g4_plan(G4Phase& ph, int first, int u1, int chun
     }
 }
 
+// Their largest, as the bits of its fp32 magnitude (any NaN: above the infinity).
+template <int XT>
+__device__ __forceinline__ uint32_t g4_x_largest(const G4Raw<XT>& r) {
+    if constexpr (XT == 1) {
+        const uint4 a = r.v[0], b = r.v[1];
+        constexpr uint32_t M = 0x7FFFFFFFu;
+        return max(max(max(a.x & M, a.y & M), max(a.z & M, a.w & M)), max(max(b.x & M, b.y & M), max(b.z & M, b.w & M)));
+    } else {   // magnitudes of 16 bits are in the order of their bits
+        const uint4 a = r.v[0];
+        constexpr uint32_t M = 0x7FFF7FFFu;
+        const uint32_t m = __vmaxu2(__vmaxu2(a.x & M, a.y & M), __vmaxu2(a.z & M, a.w & M));
+        const uint32_t h = max(m >> 16, m & 0xFFFFu);
+        if constexpr (XT == 0) return h << 16;
+        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
+    }
+}
+
 // The lane's 8 values of chunk c or c + 1 of a row of x (0 behind the last).
 template <int XT>
 __device__ __forceinline__ G4Raw<XT> g4_x_load(const G4Params& p, int row, int c0, int chunks, int c) {
@@ -418,6 +452,7 @@ __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c
     const int tile = cols * P * 64, x_chunk = g4_x_bytes(G, products, cols * P);
     // the lane's values of chunk 2i + lane / 16: columns 8l .. 8l + 7
     uint8_t* const mine = xs + (lane >> 4) * x_chunk + (l >> 2) * tile + (l & 3) * 16;
+    uint8_t* const my_sums = xs + (lane >> 4) * x_chunk + 4 * tile + l / (G / 8) * products * 32;
     auto load = [&](int col, int i) {
         return col < cols ? g4_x_load<XT>(p, ph.row[col], c0, chunks, 2 * i) : G4Raw<XT>();
     };
@@ -444,12 +479,7 @@ __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c
         const int here = col, at = i;
         next(col, i);
         const G4Raw<XT> u = load(col, i);
-        float f[8];
-        g4_x_values<XT>(v, f);
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-        m = __reduce_max_sync(0xffffffffu, m);
+        uint32_t m = __reduce_max_sync(0xffffffffu, g4_x_largest<XT>(v));
         if (lane == 0 && m) atomicMax(&ph.top[here], m);
         if (2 * at + (lane >> 4) < chunks) {
             uint8_t* bytes = mine + 2 * at * x_chunk + here * (P * 64);
@@ -481,7 +511,7 @@ __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c
         // columns 0, 1, 4, 5 times 1, columns 2, 3, 6, 7 by 16
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] *= j & 2 ? up * 0.0625f : up;
-        float* sums = reinterpret_cast<float*>(xs + (2 * i + (lane >> 4)) * x_chunk + 4 * tile) + l / (G / 8) * products * 8 + ph.sum[col];
+        float* sums = reinterpret_cast<float*>(my_sums + 2 * i * x_chunk) + ph.sum[col];
 #pragma unroll 1
         for (int q = 0; q < P; ++q) {
             uint32_t o[4];
@@ -490,11 +520,13 @@ __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c
             for (int j = 0; j < 4; ++j) {
                 const __half2 h = __floats2half2_rn(f[2 * j], f[2 * j + 1]);
                 memcpy(&o[j], &h, 4);
-                const float2 g = __half22float2(h);
-                s[j & 1] += g.x + g.y;
                 if constexpr (P > 1) {
+                    const float2 g = __half22float2(h);
+                    s[j & 1] += g.x + g.y;
                     f[2 * j] = (f[2 * j] - g.x) * 2048.f;
                     f[2 * j + 1] = (f[2 * j + 1] - g.y) * 2048.f;
+                } else {   // before rounding: the same but for what the smallest values lose, 2^-35 of the largest
+                    s[j & 1] += f[2 * j] + f[2 * j + 1];
                 }
             }
             if (in) *reinterpret_cast<uint4*>(bytes + q * 64) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -547,8 +579,8 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
     const int slots = EXPERTS ? g4_uniform(g4_rows<WARPS>(*rows, p)) : 1;
     // the CTA's units u0 .. u1 - 1
     const int groups = EXPERTS ? gridDim.x : gridDim.x / split;
-    const int total = slots * p.units, b = EXPERTS ? blockIdx.x : blockIdx.x / split, each = total / groups, more = total - each * groups;
-    const int u0 = each * b + min(b, more), u1 = u0 + each + (b < more);
+    int u0, u1;
+    g4_share(slots, groups, EXPERTS ? blockIdx.x : blockIdx.x / split, p, u0, u1);
     if (u0 == u1) return;
 
     // loads: the next chunk of this warp, in order
