@@ -661,7 +661,7 @@ class MoeLayer:
             raise RfxError(-2, f"unsupported T={T}")
         if getattr(self, "host_scratch", None) is None or self.host_scratch.numel() < nbytes:
             self.host_scratch = torch.empty(nbytes, dtype=torch.uint8, device=self.ws.device)
-            rfx_ws_init(self.host_scratch)
+            rfx_ws_init(self.host_scratch, stream)
         moe_ffn_forward_host(self.handle, x, logits, T, y, self.host_scratch, stream)
 
     def host_status(self, stream=None) -> int:

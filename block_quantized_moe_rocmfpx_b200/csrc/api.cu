@@ -31,12 +31,16 @@ struct moe_layer {
     cudaStream_t up_stream = nullptr;
     cudaEvent_t ev_free[2] = {nullptr, nullptr}, ev_ready[2] = {nullptr, nullptr};
     unsigned host_calls = 0;
+    unsigned host_inits = ~0u;   // workspaces initialised in the process as of the last call
 };
 
 namespace {
 
 bool fmt_ok(int f) { return f == 2 || f == 3 || f == 4; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+// rfx_ws_init calls so far: uploads on a layer's side stream must not pass one
+std::atomic<unsigned> ws_inits{0};
 
 int cuda_fail(const char* where, cudaError_t e) {
     return rfx_fail(RFX_ECUDA, std::string(where) + ": " + cudaGetErrorString(e));
@@ -279,6 +283,7 @@ long long debug_wait(long long dflt) {
 extern "C" int rfx_ws_init(void* ws, size_t ws_bytes, void* stream) {
     if (!ws) return rfx_fail(RFX_EINVAL, "rfx_ws_init: null workspace");
     cudaError_t e = cudaMemsetAsync(ws, 0, ws_bytes, (cudaStream_t)stream);
+    ws_inits.fetch_add(1, std::memory_order_relaxed);
     return e == cudaSuccess ? RFX_OK : cuda_fail("rfx_ws_init", e);
 }
 
@@ -517,7 +522,15 @@ extern "C" int moe_ffn_forward_host(const moe_layer* layer, const void* x, const
     void* xd = b + S.x[s];
     float* ld = (float*)(b + S.logits[s]);
     // uploads: on the side stream once the kernels of the call that used this
-    // buffer set two calls ago have read it; `stream` waits for them
+    // buffer set two calls ago have read it; `stream` waits for them.  A scratch that may
+    // be new or zeroed since the last call first waits for what `stream` holds (the memset,
+    // and earlier work of the memory)
+    const unsigned inits = ws_inits.load(std::memory_order_relaxed);
+    if (side && inits != L->host_inits) {
+        for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = cudaEventRecord(L->ev_free[i], st);
+        if (e != cudaSuccess) return cuda_fail("moe_ffn_forward_host", e);
+        L->host_inits = inits;
+    }
     cudaStream_t us = side ? L->up_stream : st;
     if (side) e = cudaStreamWaitEvent(us, L->ev_free[s], 0);
     if (e == cudaSuccess) e = cudaMemcpyAsync(xd, x, (size_t)T * d.H * 2, cudaMemcpyHostToDevice, us);

@@ -292,6 +292,30 @@ def test_forward_host_pageable_buffers(full_layer):
     assert torch.equal(yh, y.cpu())
 
 
+@pytest.mark.parametrize("again", [False, True])
+def test_forward_host_behind_a_busy_stream(full_layer, again):
+    """The scratch's zeroing still waits on the stream when the uploads are issued: they must not
+    pass it, on a layer's first call or after the scratch was initialised again."""
+    ml = full_layer.moe_layer()
+    T = 3
+    L = synth.logits(10, 0, 5, T, 256, 1.1)
+    xb = synth.x_bf16(10, 5, T, 4096)
+    x, l = torch.from_numpy(xb).view(torch.bfloat16).pin_memory(), torch.from_numpy(L).pin_memory()
+    want, y = (torch.full((T, 4096), float("nan")).pin_memory() for _ in range(2))
+    full_layer.moe_layer().forward_host(x, l, want)
+    torch.cuda.synchronize()
+    if again:
+        ml.forward_host(x, l, y)
+        torch.cuda.synchronize()
+        y.fill_(float("nan"))
+    torch.cuda._sleep(100_000_000)
+    if again:
+        rfx.rfx_ws_init(ml.host_scratch)
+    ml.forward_host(x, l, y)
+    torch.cuda.synchronize()
+    assert bool((want != 0).any()) and torch.equal(y, want)
+
+
 def test_forward_host_mixed_paths(full_layer):
     """Back-to-back host-buffer calls on one layer that alternate the buffer
     kinds: all page-locked (y stored by the kernel straight into host memory),
