@@ -26,7 +26,7 @@
 //
 // Bound at large sizes by memory (G = 128, q = 1: 4.8 TB/s of weights) with the instruction slots close
 // behind (G = 64, zeros, q = 4: 40 instructions per 16 x 32 weights, 68 % of the issue slots); at small ones by the
-// launch and its start (4 us for one 32 x 128 matrix).
+// launch and its start (3 us for one 64 x 512 matrix).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -421,80 +421,99 @@ __device__ __forceinline__ uint32_t g4_x_largest(const G4Raw<XT>& r) {
     }
 }
 
-// The lane's 8 values of chunk c or c + 1 of a row of x (0 behind the last).
-template <int XT>
-__device__ __forceinline__ G4Raw<XT> g4_x_load(const G4Params& p, int row, int c0, int chunks, int c) {
-    const int lane = threadIdx.x & 31;
-    G4Raw<XT> r = {};
-    c += lane >> 4;
-    const int k = (c0 + c) * G4_CHUNK + (lane & 15) * 8;
-    if (c < chunks && k < p.K) {
-        const uint4* src = reinterpret_cast<const uint4*>((const uint8_t*)p.x + ((long long)row * p.K + k) * G4X<XT>::BYTES);
-        r.v[0] = __ldg(src);
-        if constexpr (XT == 1) r.v[1] = __ldg(src + 1);
+// Where a lane works while x is staged: a warp takes two chunks of a column at a time, all pairs of all columns
+// in turn, a lane 8 values (its place of 16 bytes, or two of a column's three for fp32).
+template <int XT, bool EXPERTS, int WARPS>
+struct G4XPlace {
+    int col, i, pairs, turn_col, turn_i;
+    __device__ __forceinline__ explicit G4XPlace(int chunks) {
+        const int warp = g4_uniform(threadIdx.x >> 5);
+        pairs = (chunks + 1) >> 1;
+        if constexpr (EXPERTS) {   // on the path of their start, and short of registers (one token's gate/up: 16.6 / 17.2 us)
+            col = 0;
+            i = warp - WARPS;
+            next();
+        } else {
+            col = warp / pairs;
+            i = warp - col * pairs;
+            turn_col = WARPS / pairs;
+            turn_i = WARPS - turn_col * pairs;
+        }
     }
-    return r;
-}
+    __device__ __forceinline__ void next() {
+        if constexpr (EXPERTS) {
+            i += WARPS;
+            while (i >= pairs) {
+                i -= pairs;
+                ++col;
+            }
+        } else {
+            i += turn_i;
+            const int over = i >= pairs;
+            i -= over ? pairs : 0;
+            col += turn_col + over;
+        }
+    }
+    // the lane's 8 values of chunk 2i or 2i + 1 of a row of x (0 behind the last)
+    __device__ __forceinline__ G4Raw<XT> load(const G4Params& p, int row, int c0, int chunks) const {
+        const int lane = threadIdx.x & 31, c = 2 * i + (lane >> 4), k = (c0 + c) * G4_CHUNK + (lane & 15) * 8;
+        G4Raw<XT> r = {};
+        if (c < chunks && k < p.K) {
+            const uint4* src = reinterpret_cast<const uint4*>((const uint8_t*)p.x + ((long long)row * p.K + k) * G4X<XT>::BYTES);
+            r.v[0] = __ldg(src);
+            if constexpr (XT == 1) r.v[1] = __ldg(src + 1);
+        }
+        return r;
+    }
+};
 
 // One matrix: a warp's first part of x, asked for before anything else.
-template <int XT> struct G4XFirst { int col, i; G4Raw<XT> v; };
+template <int XT, int WARPS> struct G4XFirst { G4XPlace<XT, false, WARPS> at; G4Raw<XT> v; };
 
 // x of the planned columns into shared memory, by all warps: first as it is (the next part on its way
 // while one is looked at for its largest value), then in place as the products take it.
-// A warp takes two chunks of a column at a time, a lane 8 values.  Each turn is a chain of dependent
-// steps (about 1100 cycles to the first values from memory, then several hundred a turn), so few wide turns win:
-// 4096 x 4096, q = 8, 11.1 us against 14.2 with one chunk and 4 values a lane; q = 1, 6.7 against 7.0.
-template <int XT, int G, bool Z, int WARPS>
-__device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c0, int chunks, uint8_t* xs, const G4XFirst<XT>* begun) {
+// The instruction slots bound it (about 100 a warp and turn, of either pass), and behind them the chain of a turn: few
+// wide turns win (two chunks and 8 values a lane against one and 4, 4096 x 4096, q = 8: 11.1 / 14.2 us).
+template <int XT, int G, bool Z, bool EXPERTS, int WARPS>
+__device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c0, int chunks, uint8_t* xs, const G4XFirst<XT, WARPS>* begun) {
+    using Place = G4XPlace<XT, EXPERTS, WARPS>;
     constexpr int P = G4X<XT>::PARTS;
-    const int lane = threadIdx.x & 31, warp = g4_uniform(threadIdx.x >> 5), l = lane & 15;
-    const int cols = g4_uniform(ph.cols), products = g4_uniform(ph.products), pairs = (chunks + 1) >> 1;
+    const int lane = threadIdx.x & 31, l = lane & 15;
+    const int cols = EXPERTS ? g4_uniform(ph.cols) : p.R, products = g4_uniform(ph.products);
     const int tile = cols * P * 64, x_chunk = g4_x_bytes(G, products, cols * P);
     // the lane's values of chunk 2i + lane / 16: columns 8l .. 8l + 7
     uint8_t* const mine = xs + (lane >> 4) * x_chunk + (l >> 2) * tile + (l & 3) * 16;
     uint8_t* const my_sums = xs + (lane >> 4) * x_chunk + 4 * tile + l / (G / 8) * products * 32;
-    auto load = [&](int col, int i) {
-        return col < cols ? g4_x_load<XT>(p, ph.row[col], c0, chunks, 2 * i) : G4Raw<XT>();
+    auto load = [&](const Place& at) {
+        return at.col < cols ? at.load(p, EXPERTS ? ph.row[at.col] : at.col, c0, chunks) : G4Raw<XT>();
     };
-    auto next = [&](int& col, int& i) {
-        i += WARPS;
-        while (i >= pairs) {
-            i -= pairs;
-            ++col;
-        }
+    auto start = [&]() {
+        if constexpr (EXPERTS) return Place(chunks);
+        else return begun->at;
     };
-    int col = 0, i = warp - WARPS;
+    Place at = start();
     G4Raw<XT> v;
-    if (begun) {
-        col = begun->col;
-        i = begun->i;
-        v = begun->v;
-    } else {
-        next(col, i);
-        v = load(col, i);
-    }
-    const int col1 = col, i1 = i;
+    if constexpr (EXPERTS) v = load(at);
+    else v = begun->v;
 #pragma unroll 1
-    while (col < cols) {
-        const int here = col, at = i;
-        next(col, i);
-        const G4Raw<XT> u = load(col, i);
-        uint32_t m = __reduce_max_sync(0xffffffffu, g4_x_largest<XT>(v));
+    while (at.col < cols) {
+        const int here = at.col, i = at.i;
+        at.next();
+        const G4Raw<XT> u = load(at);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, g4_x_largest<XT>(v));
         if (lane == 0 && m) atomicMax(&ph.top[here], m);
-        if (2 * at + (lane >> 4) < chunks) {
-            uint8_t* bytes = mine + 2 * at * x_chunk + here * (P * 64);
+        if (2 * i + (lane >> 4) < chunks) {
+            uint8_t* bytes = mine + i * 2 * x_chunk + here * (P * 64);
             *reinterpret_cast<uint4*>(bytes) = v.v[0];
             if constexpr (XT == 1) *reinterpret_cast<uint4*>(bytes + 64) = v.v[1];
         }
         v = u;
     }
     __syncthreads();
-    col = col1;
-    i = i1;
 #pragma unroll 1
-    while (col < cols) {
-        const bool in = 2 * i + (lane >> 4) < chunks;
-        uint8_t* bytes = mine + 2 * i * x_chunk + col * (P * 64);
+    for (at = start(); at.col < cols; at.next()) {
+        const bool in = 2 * at.i + (lane >> 4) < chunks;
+        uint8_t* bytes = mine + at.i * 2 * x_chunk + at.col * (P * 64);
         G4Raw<XT> r = {};
         if (in) {
             r.v[0] = *reinterpret_cast<const uint4*>(bytes);
@@ -502,16 +521,16 @@ __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c
         }
         float f[8];
         g4_x_values<XT>(r, f);
-        const uint32_t top = ph.top[col];
+        const uint32_t top = ph.top[at.col];
         // the largest lands in [2^13, 2^14); at most 2^126, which still keeps the smallest columns whole
         const int E = min(126, 13 + 127 - (int)(top >> 23));
         const float up = __uint_as_float((uint32_t)(127 + E) << 23);
-        if (i == 0 && lane == 0)
-            ph.down[col] = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : (uint32_t)(127 - E) << 23);
+        if (at.i == 0 && lane == 0)
+            ph.down[at.col] = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : (uint32_t)(127 - E) << 23);
         // columns 0, 1, 4, 5 times 1, columns 2, 3, 6, 7 by 16
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] *= j & 2 ? up * 0.0625f : up;
-        float* sums = reinterpret_cast<float*>(my_sums + 2 * i * x_chunk) + ph.sum[col];
+        float* sums = reinterpret_cast<float*>(my_sums + at.i * 2 * x_chunk) + ph.sum[at.col];
 #pragma unroll 1
         for (int q = 0; q < P; ++q) {
             uint32_t o[4];
@@ -535,7 +554,6 @@ __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c
             for (int d = 1; d < G / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             if (in && l % (G / 8) == 0) sums[q] = sum * (Z ? -0x1.0p-21f : -0x1.0p-18f);
         }
-        next(col, i);
     }
     __syncthreads();
 }
@@ -645,16 +663,14 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
         fstage ^= STAGE;
     };
     if (fl) aim();
-    G4XFirst<XT> begun;
+    G4XFirst<XT, WARPS> begun = {G4XPlace<XT, false, WARPS>(chunks), {}};   // (experts: not used, and gone)
     if constexpr (!EXPERTS) {
         // One matrix: all up to here may run beside the kernel before (512 x 2048: 4.8 -> 4.3 us; the weights' way
         // into the L2 from here on too: 0.1 us slower).
         grid_dep_wait();
-        // the warp's first part of x, on its way while the rest is set up
-        const int pairs = (chunks + 1) >> 1;
-        begun.col = warp / pairs;
-        begun.i = warp - begun.col * pairs;
-        begun.v = begun.col < p.R ? g4_x_load<XT>(p, begun.col, c0, chunks, 2 * begun.i) : G4Raw<XT>();
+        // the warp's first part of x, on its way while the rest is set up (x by asynchronous copies ahead of the
+        // weights: 4096 x 4096, q = 8, 11.8 / 10.3 us)
+        if (begun.at.col < p.R) begun.v = begun.at.load(p, begun.at.col, c0, chunks);
     }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) fetch();
@@ -746,7 +762,7 @@ __global__ void __launch_bounds__(g4_warps(NBMAX) * 32, 1) g4_kernel(G4Params p)
         products = g4_uniform(ph.products);
         tile = g4_uniform(ph.cols) * P * 64;
         x_chunk = g4_x_bytes(G, products, g4_uniform(ph.cols) * P);
-        g4_stage_x<XT, G, Z, WARPS>(p, ph, c0, chunks, xs, EXPERTS ? nullptr : &begun);
+        g4_stage_x<XT, G, Z, EXPERTS, WARPS>(p, ph, c0, chunks, xs, EXPERTS ? nullptr : &begun);
         const bool done = !EXPERTS || phase_end * (long long)p.units >= u1;   // the CTA's last slots
 #pragma unroll 1
         while (true) {
