@@ -327,7 +327,8 @@ int rfx_g4_pack_device(const uint8_t* codes, const uint16_t* scales, const uint8
  * magnitude to [2^13, 2^14): bf16 and fp16 values are whole down to 2^-23 of the largest and
  * within 2^-35 of the largest below that; fp32 values enter as three such parts (33 bits).
  * The products code * x are exact; each group's sum, code * x minus zero * sum of x, is taken in
- * fp32, scaled and added in fp32.  The order of the sums depends on the shapes only, so results repeat bit for bit.
+ * fp32, scaled and added in fp32.  The order of the sums depends on N, K and the
+ * GPU only (fp32 x: and on q > 2; K in parts: on q), so results repeat bit for bit, whatever the other columns hold.
  * A column of x with an infinity or a NaN gives NaN, and no other column does.
  * Limits: 1 <= q <= 8, N >= 1, K % group == 0.  No workspace.  One launch; more where the
  * columns' x does not fit shared memory (about q * K > 45,000 for 16-bit x, 14,000 for fp32) or fp32 x has more than
@@ -481,7 +482,7 @@ int moe_ffn_forward_logits(const moe_layer* layer, const void* x, int T, const f
  * everything stays on `stream`.  Calls on one layer are serialised by a lock
  * in the layer.  scratch: device, 256-byte aligned,
  * moe_ffn_host_scratch_bytes(layer, T) bytes, caller-owned, zeroed once with
- * rfx_ws_init before its first use; it holds the moe_ffn_forward workspace
+ * rfx_ws_init (on `stream`, or finished) before its first use; it holds the moe_ffn_forward workspace
  * first (so rfx_ws_status(scratch) reads its device flag), then the device
  * copies and the routing.  T > 8 runs the prefill path.
  */
