@@ -139,6 +139,20 @@ def test_gemv_of_several_parts_of_K(dtype, q, zeros, chunks):
         check(y, w.dense(), x, G, integer=True)
 
 
+@pytest.mark.parametrize("N", [1180, 2400, 4800])
+@pytest.mark.parametrize("dtype,q", [(BF, 8), (FF, 8), (FF, 2)])
+def test_gemv_of_many_rows_and_several_parts_of_K(N, dtype, q):
+    # as above without clusters, or in narrow ones: parts of about 44 (fp32, q = 2: 58) chunks a CTA
+    G = 128
+    for n in (45, 89, 90, 133):
+        K = 128 * n
+        w = G4(N, K, G, True, n, integer=True)
+        x = x_of((q, K), dtype, n, True)
+        y = torch.full((q, N), float("nan"), device=DEV)
+        rfx.rfx_gemv_g4(w.packed, N, K, G, x, y, zeros=True)
+        check(y, w.dense(), x, G, integer=True)
+
+
 @pytest.mark.parametrize("N,K", [(40, 4096), (500, 14336), (800, 8192), (1400, 4096), (4096, 2048)])
 def test_gemv_columns_are_independent_in_clusters(N, K):
     w = G4(N, K, 64, False, 6)
