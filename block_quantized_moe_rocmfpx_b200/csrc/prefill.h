@@ -11,13 +11,14 @@
 
 // workspace control words (uint32 index).  Word 2 is the device error flag,
 // at the same place as in the decode workspace so that one status call reads
-// both.
+// both.  The block is as long as decode's, whose counters (words 64 on) have to
+// be zero when a decode call follows on the same workspace: nothing is written there.
 #define PF_CTRL_ERR 2
 #define PF_CTRL_NTILES 8     // token tiles (written by the grouping)
 #define PF_CTRL_ROWS 9       // routed rows (sum of the per-expert counts)
 #define PF_CTRL_NEXT0 10     // next unit to hand out, gate/up GEMM (reset by the grouping)
 #define PF_CTRL_NEXT1 11     // next unit to hand out, down GEMM
-#define PF_CTRL_WORDS 64
+#define PF_CTRL_WORDS MOE_CTRL_WORDS
 
 #define PF_TILE_N 256        // most tokens per token tile (the MMA's largest N)
 #define PF_BM 128            // weight rows per tile (the MMA's M)

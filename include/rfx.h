@@ -412,7 +412,8 @@ int moe_layer_create_mix(const moe_layer_desc* d, const moe_expert_mix* mix, moe
  * the prefill workspace, moe_prefill_workspace_bytes).  The
  * workspace holds counters, the SwiGLU intermediate and per-expert partial
  * outputs; it must be zeroed once (rfx_ws_init) before its first use and may
- * then be reused by successive calls on the same stream.  Calls that overlap
+ * then be reused by successive calls on the same stream, of any T that it is
+ * large enough for, decode and prefill in any order.  Calls that overlap
  * on the GPU must use different workspaces.
  */
 size_t moe_ffn_workspace_bytes(const moe_layer* layer, int T);

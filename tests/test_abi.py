@@ -303,6 +303,26 @@ def test_host_call_scratch_bytes():
         rfx.moe_layer_destroy(h)
 
 
+def test_prefill_workspace_leaves_the_decode_control_words_alone():
+    """A workspace may be used by calls of any T in turn.  The decode kernel's control words (1024 bytes: the
+    counters of its slots lie at bytes 256 .. 515) have to be zero when it starts, so no section that a prefill
+    call writes may lie there; the first one is the counts."""
+    d = rfx.moe_layer_desc()
+    d.H, d.I, d.E, d.k = 512, 256, 16, 4
+    d.f_gate, d.f_up, d.f_down = 2, 2, 3
+    d.gate = d.up = d.down = 256
+    d.stride_gate = d.stride_up = rfx.rfx_packed_bytes(2, 256, 512)
+    d.stride_down = rfx.rfx_packed_bytes(3, 512, 256)
+    h = rfx.moe_layer_create(d)
+    try:
+        v = rfx.moe_prefill_ws_view()
+        assert rfx._pf_view(h, 40, 4096, ctypes.byref(v)) == rfx.RFX_OK
+        for field in ("counts", "row_token", "row_weight", "h"):
+            assert getattr(v, field) >= 4096 + 1024, field
+    finally:
+        rfx.moe_layer_destroy(h)
+
+
 def test_fault_hook_rejects_bad_arguments():
     with pytest.raises(rfx.RfxError):
         rfx.rfx_debug_set_fault(7, 0)

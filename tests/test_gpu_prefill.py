@@ -223,6 +223,39 @@ def test_forward_dispatches_large_T_to_prefill():
     torch.testing.assert_close(y1, y2, rtol=1e-6, atol=1e-6 * float(y2.abs().max()))
 
 
+@pytest.mark.parametrize("exact", [False, True])
+def test_decode_after_prefill_on_one_workspace(exact):
+    """Successive calls of any T may use one workspace: a decode call behind a prefill (whose counts by expert
+    are far above the I / 32 = 8 units that a slot's counter waits for) gives the bits of a fresh workspace."""
+    H, I, E, k = 512, 256, 8, 4
+    lay = SynthLayer(57, 0, H, I, E, k)
+    big = 300
+    ml = lay.moe_layer()
+    prec = rfx.RFX_PREFILL_EXACT if exact else rfx.RFX_PREFILL_BF16
+    ws = torch.empty(max(rfx.moe_prefill_workspace_bytes_ex(ml.handle, big, prec),
+                         rfx.moe_ffn_workspace_bytes(ml.handle, 8)), dtype=torch.uint8, device=DEV)
+    rfx.rfx_ws_init(ws)
+
+    def inputs(T, seed):
+        idx = torch.empty((T, k), dtype=torch.int32, device=DEV)
+        w = torch.empty((T, k), dtype=torch.float32, device=DEV)
+        rfx.moe_router_topk(to_dev(synth.logits(57, 0, seed, T, E, 0.0)), k, idx, w)
+        return to_dev(synth.x_bf16(57, seed, T, H), torch.bfloat16), idx, w
+
+    xp, ip, wp = inputs(big, 0)
+    yp = torch.empty((big, H), dtype=torch.float32, device=DEV)
+    for i, T in enumerate((1, 8, 3, 8)):
+        x, idx, w = inputs(T, 400 + 10 * i)
+        want, y = (torch.full((T, H), float("nan"), device=DEV) for _ in range(2))
+        ml.ws.zero_()
+        rfx.moe_ffn_forward(ml.handle, x, T, idx, w, want, ml.ws)
+        rfx.moe_ffn_prefill_ex(ml.handle, xp, big, ip, wp, yp, ws, prec)
+        rfx.moe_ffn_forward(ml.handle, x, T, idx, w, y, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), T
+    assert rfx.rfx_ws_status(ws) == rfx.RFX_OK
+
+
 def test_prefill_bad_expert_ids_set_the_device_flag():
     lay = SynthLayer(59, 0, 512, 256, 8, 2)
     ml = lay.moe_layer()
