@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <map>
 #include <mutex>
 #include <new>
 #include <string>
@@ -32,6 +33,7 @@ struct moe_layer {
     cudaEvent_t ev_free[2] = {nullptr, nullptr}, ev_ready[2] = {nullptr, nullptr};
     unsigned host_calls = 0;
     unsigned host_inits = ~0u;   // workspaces initialised in the process as of the last call
+    const void* host_scratch = nullptr;   // the scratch that ev_free speaks of: that of the last call
 };
 
 namespace {
@@ -41,6 +43,45 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // rfx_ws_init calls so far: uploads on a layer's side stream must not pass one
 std::atomic<unsigned> ws_inits{0};
+
+// The last host call on each scratch: the buffer sets lie where its layer's sizes and its T put them, and
+// ev_free of that layer says when its kernels have read them.
+struct HostUse {
+    const moe_layer* layer;
+    int T;
+    bool captured;   // a captured call used the scratch: a replay may at any time
+};
+std::mutex host_uses_mu;
+std::map<const void*, HostUse>& host_uses() {
+    static auto* uses = new std::map<const void*, HostUse>;   // for as long as the process: layers may go last
+    return *uses;
+}
+
+// Note a call on a scratch.  `known`: the events of the layer cover all that may still use the scratch, as
+// the call before was the layer's own with the same T.
+int host_use(const moe_layer* L, const void* scratch, int T, bool captured, bool& known) {
+    try {
+        std::lock_guard<std::mutex> lock(host_uses_mu);
+        HostUse& u = host_uses().try_emplace(scratch, HostUse{nullptr, 0, false}).first->second;
+        known = u.layer == L && u.T == T && !u.captured && L->host_scratch == scratch;
+        u = HostUse{L, T, u.captured || captured};
+        return RFX_OK;
+    } catch (...) {
+        return rfx_fail(RFX_EINVAL, "moe_ffn_forward_host: out of host memory");
+    }
+}
+
+// A layer goes: what is left of its uses says nothing any more (a captured one's scratch may still be replayed).
+void host_uses_end(const moe_layer* L) {
+    try {
+        std::lock_guard<std::mutex> lock(host_uses_mu);
+        for (auto it = host_uses().begin(); it != host_uses().end();) {
+            if (it->second.layer == L) it->second.layer = nullptr;
+            it = it->second.layer || it->second.captured ? std::next(it) : host_uses().erase(it);
+        }
+    } catch (...) {   // the map could not be made: it holds nothing
+    }
+}
 
 int cuda_fail(const char* where, cudaError_t e) {
     return rfx_fail(RFX_ECUDA, std::string(where) + ": " + cudaGetErrorString(e));
@@ -231,6 +272,7 @@ extern "C" int moe_layer_create_mix(const moe_layer_desc* d, const moe_expert_mi
 
 extern "C" void moe_layer_destroy(moe_layer* layer) {
     if (!layer) return;
+    host_uses_end(layer);
     if (layer->mix_dev) cudaFree(layer->mix_dev);
     for (int i = 0; i < 2; ++i) {
         if (layer->ev_free[i]) cudaEventDestroy(layer->ev_free[i]);
@@ -518,18 +560,24 @@ extern "C" int moe_ffn_forward_host(const moe_layer* layer, const void* x, const
         e = host_streams(L);
         if (e != cudaSuccess) return cuda_fail("moe_ffn_forward_host", e);
     }
+    bool known = false;
+    int rc = host_use(L, scratch, T, !side, known);
+    if (rc != RFX_OK) return rc;
     const int s = side ? (int)(L->host_calls++ & 1u) : 0;
     void* xd = b + S.x[s];
     float* ld = (float*)(b + S.logits[s]);
     // uploads: on the side stream once the kernels of the call that used this
     // buffer set two calls ago have read it; `stream` waits for them.  A scratch that may
-    // be new or zeroed since the last call first waits for what `stream` holds (the memset,
-    // and earlier work of the memory)
+    // be new or zeroed since the last call, or that was last used otherwise (another layer, T
+    // or a graph: its sets may lie in what that call still works with), first waits for what
+    // `stream` holds
     const unsigned inits = ws_inits.load(std::memory_order_relaxed);
-    if (side && inits != L->host_inits) {
+    if (side && (!known || inits != L->host_inits)) {
+        L->host_scratch = nullptr;
         for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = cudaEventRecord(L->ev_free[i], st);
         if (e != cudaSuccess) return cuda_fail("moe_ffn_forward_host", e);
         L->host_inits = inits;
+        L->host_scratch = scratch;
     }
     cudaStream_t us = side ? L->up_stream : st;
     if (side) e = cudaStreamWaitEvent(us, L->ev_free[s], 0);
@@ -549,7 +597,7 @@ extern "C" int moe_ffn_forward_host(const moe_layer* layer, const void* x, const
         else
             (void)cudaGetLastError();   // not an error: pageable memory takes the copy below
     }
-    int rc = moe_ffn_forward_logits(layer, xd, T, ld, idx, w, ydev ? ydev : yd, b + S.ffn, S.x[0], stream);
+    rc = moe_ffn_forward_logits(layer, xd, T, ld, idx, w, ydev ? ydev : yd, b + S.ffn, S.x[0], stream);
     if (rc != RFX_OK) return rc;
     if (side) {
         e = cudaEventRecord(L->ev_free[s], st);

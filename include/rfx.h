@@ -476,15 +476,17 @@ int moe_ffn_forward_logits(const moe_layer* layer, const void* x, int T, const f
  * copies to be asynchronous).  The two uploads run on a stream the layer
  * makes on first use, into one of two buffer sets used in turn, and `stream`
  * waits for them: a call's uploads overlap the kernels of the call before
- * it.  The kernels and the download run on `stream`; x, the logits and y may
+ * it, where the scratch's last call was the same layer's with the same T.  Otherwise (another T, another
+ * layer, a scratch that a captured call uses too) they wait for what `stream` holds at the call.  The kernels and the download run on `stream`; x, the logits and y may
  * be reused once `stream` has synchronised.  For T <= 8 a y in page-locked
  * host memory that the device can address (cudaHostAlloc, cudaHostRegister)
  * receives the decode kernel's stores directly instead of a copy.  Inside a CUDA graph capture
  * everything stays on `stream`.  Calls on one layer are serialised by a lock
  * in the layer.  scratch: device, 256-byte aligned,
  * moe_ffn_host_scratch_bytes(layer, T) bytes, caller-owned, zeroed once with
- * rfx_ws_init (on `stream`, or finished) before its first use; it holds the moe_ffn_forward workspace
- * first (so rfx_ws_status(scratch) reads its device flag), then the device
+ * rfx_ws_init (on `stream`, or finished) before its first use; calls of any layer and of any T that it is large
+ * enough for may use it in turn, but may not overlap on the GPU, nor may anything else write to it.  It
+ * holds the moe_ffn_forward workspace first (so rfx_ws_status(scratch) reads its device flag), then the device
  * copies and the routing.  T > 8 runs the prefill path.
  */
 size_t moe_ffn_host_scratch_bytes(const moe_layer* layer, int T);
