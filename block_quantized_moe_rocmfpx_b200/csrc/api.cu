@@ -32,7 +32,6 @@ struct moe_layer {
     cudaStream_t up_stream = nullptr;
     cudaEvent_t ev_free[2] = {nullptr, nullptr}, ev_ready[2] = {nullptr, nullptr};
     unsigned host_calls = 0;
-    unsigned host_inits = ~0u;   // workspaces initialised in the process as of the last call
     const void* host_scratch = nullptr;   // the scratch that ev_free speaks of: that of the last call
 };
 
@@ -41,14 +40,12 @@ namespace {
 bool fmt_ok(int f) { return f == 2 || f == 3 || f == 4; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-// rfx_ws_init calls so far: uploads on a layer's side stream must not pass one
-std::atomic<unsigned> ws_inits{0};
-
-// The last host call on each scratch: the buffer sets lie where its layer's sizes and its T put them, and
-// ev_free of that layer says when its kernels have read them.
+// The last host call on each scratch since it was zeroed: the buffer sets lie where its layer's
+// sizes and its T put them, and ev_free of that layer says when its kernels have read them.
 struct HostUse {
-    const moe_layer* layer;
+    const moe_layer* layer;   // null: zeroed since, or the layer is gone
     int T;
+    size_t bytes;    // of the scratch that the call uses
     bool captured;   // a captured call used the scratch: a replay may at any time
 };
 std::mutex host_uses_mu;
@@ -59,15 +56,26 @@ std::map<const void*, HostUse>& host_uses() {
 
 // Note a call on a scratch.  `known`: the events of the layer cover all that may still use the scratch, as
 // the call before was the layer's own with the same T.
-int host_use(const moe_layer* L, const void* scratch, int T, bool captured, bool& known) {
+int host_use(const moe_layer* L, const void* scratch, int T, size_t bytes, bool captured, bool& known) {
     try {
         std::lock_guard<std::mutex> lock(host_uses_mu);
-        HostUse& u = host_uses().try_emplace(scratch, HostUse{nullptr, 0, false}).first->second;
+        HostUse& u = host_uses().try_emplace(scratch, HostUse{nullptr, 0, 0, false}).first->second;
         known = u.layer == L && u.T == T && !u.captured && L->host_scratch == scratch;
-        u = HostUse{L, T, u.captured || captured};
+        u = HostUse{L, T, std::max(u.bytes, bytes), u.captured || captured};
         return RFX_OK;
     } catch (...) {
         return rfx_fail(RFX_EINVAL, "moe_ffn_forward_host: out of host memory");
+    }
+}
+
+// Memory is zeroed: uploads into a scratch there must not pass that.
+void host_uses_zeroed(const void* ws, size_t bytes) {
+    const uintptr_t a = (uintptr_t)ws;
+    try {
+        std::lock_guard<std::mutex> lock(host_uses_mu);
+        for (auto& [scratch, u] : host_uses())
+            if ((uintptr_t)scratch < a + bytes && a < (uintptr_t)scratch + u.bytes) u.layer = nullptr;
+    } catch (...) {   // the map could not be made: it holds nothing
     }
 }
 
@@ -325,7 +333,7 @@ long long debug_wait(long long dflt) {
 extern "C" int rfx_ws_init(void* ws, size_t ws_bytes, void* stream) {
     if (!ws) return rfx_fail(RFX_EINVAL, "rfx_ws_init: null workspace");
     cudaError_t e = cudaMemsetAsync(ws, 0, ws_bytes, (cudaStream_t)stream);
-    ws_inits.fetch_add(1, std::memory_order_relaxed);
+    host_uses_zeroed(ws, ws_bytes);
     return e == cudaSuccess ? RFX_OK : cuda_fail("rfx_ws_init", e);
 }
 
@@ -561,7 +569,7 @@ extern "C" int moe_ffn_forward_host(const moe_layer* layer, const void* x, const
         if (e != cudaSuccess) return cuda_fail("moe_ffn_forward_host", e);
     }
     bool known = false;
-    int rc = host_use(L, scratch, T, !side, known);
+    int rc = host_use(L, scratch, T, S.total, !side, known);
     if (rc != RFX_OK) return rc;
     const int s = side ? (int)(L->host_calls++ & 1u) : 0;
     void* xd = b + S.x[s];
@@ -571,12 +579,10 @@ extern "C" int moe_ffn_forward_host(const moe_layer* layer, const void* x, const
     // be new or zeroed since the last call, or that was last used otherwise (another layer, T
     // or a graph: its sets may lie in what that call still works with), first waits for what
     // `stream` holds
-    const unsigned inits = ws_inits.load(std::memory_order_relaxed);
-    if (side && (!known || inits != L->host_inits)) {
+    if (side && !known) {
         L->host_scratch = nullptr;
         for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = cudaEventRecord(L->ev_free[i], st);
         if (e != cudaSuccess) return cuda_fail("moe_ffn_forward_host", e);
-        L->host_inits = inits;
         L->host_scratch = scratch;
     }
     cudaStream_t us = side ? L->up_stream : st;

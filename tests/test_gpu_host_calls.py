@@ -153,3 +153,36 @@ def test_one_layer_on_two_streams_with_a_scratch_each():
     torch.cuda.synchronize()
     for x, logits, y in ins:
         check(ml, x, logits, y)
+
+
+@pytest.mark.parametrize("part", [None, "all", "end"])
+def test_uploads_run_ahead_unless_the_scratch_itself_was_zeroed(part):
+    # behind a busy stream: a workspace of something else that is zeroed does not hold the uploads up, the
+    # scratch (or a part of it) does
+    _, (ml,) = layers(1)
+    T = 4
+    scratch = scratch_for(ml, T)
+    other = torch.empty(4096, dtype=torch.uint8, device=DEV)
+    ins = [host_inputs(T, 1500 + 23 * i) for i in range(3)]
+    for x, logits, y in ins[:2]:
+        rfx.moe_ffn_forward_host(ml.handle, x, logits, T, y, scratch)
+    torch.cuda.synchronize()
+    x, logits, y = ins[2]
+    at = (rfx.moe_ffn_workspace_bytes(ml.handle, T) + 255) // 256 * 256      # the first set's x: the third call's
+    there = scratch[at:at + 2 * T * H].view(torch.bfloat16).view(T, H)
+    assert not torch.equal(there.cpu(), x)
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(8 * BUSY)
+    done.record()
+    rfx.rfx_ws_init(other if part is None else scratch if part == "all" else scratch[-256:])
+    rfx.moe_ffn_forward_host(ml.handle, x, logits, T, y, scratch)
+    seen, copy = False, torch.empty((T, H), dtype=torch.bfloat16).pin_memory()
+    while not seen and not done.query():
+        with torch.cuda.stream(side):
+            copy.copy_(there, non_blocking=True)
+        side.synchronize()
+        seen = torch.equal(copy, x) and not done.query()
+    torch.cuda.synchronize()
+    assert seen == (part is None)
+    check(ml, x, logits, y)
