@@ -819,6 +819,17 @@ inline int g4_team(long long units, int chunks, int sms, int warps) {
     return best;
 }
 
+// Shared memory of a CTA beside x, and what is left for x.
+template <int G, bool Z, int MODE, int NBMAX>
+constexpr int g4_fixed() {
+    constexpr int WARPS = g4_warps(NBMAX), FULL = g4_chunk_bytes(G4_CHUNK, G, Z);
+    return WARPS * 1024 + WARPS * 2 * G4_NR * FULL + (MODE ? (int)sizeof(G4Rows) : 0);
+}
+template <int G, bool Z, int MODE, int NBMAX>
+constexpr int g4_room() {   // less the kernel's static part
+    return (G4_SMEM - (int)sizeof(G4Phase) - g4_warps(NBMAX) * 64 - (MODE ? 0 : G4_SPLIT * 1024) - 640 - g4_fixed<G, Z, MODE, NBMAX>()) & ~127;
+}
+
 template <int XT, int G, bool Z, int MODE, int NBMAX>
 cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
     constexpr bool EXPERTS = MODE > 0, PAIR = MODE == 2;
@@ -826,9 +837,7 @@ cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
     cudaError_t e = device_sms(sms);
     if (e != cudaSuccess) return e;
     constexpr int P = G4X<XT>::PARTS, CO = G4X<XT>::COLS, WARPS = g4_warps(NBMAX);
-    constexpr int FULL = g4_chunk_bytes(G4_CHUNK, G, Z);
-    const int fixed = WARPS * 1024 + WARPS * 2 * G4_NR * FULL + (EXPERTS ? (int)sizeof(G4Rows) : 0);
-    const int room = (G4_SMEM - (int)sizeof(G4Phase) - WARPS * 64 - (EXPERTS ? 0 : G4_SPLIT * 1024) - 640 - fixed) & ~127;   // less the kernel's static part
+    constexpr int fixed = g4_fixed<G, Z, MODE, NBMAX>(), room = g4_room<G, Z, MODE, NBMAX>();
     p.rg_bytes = g4_rowgroup_bytes(p.K, G, Z);
     p.units = PAIR ? (p.N + 15) / 16 : (p.N + 31) / 32;
     const int chunks = (p.K + G4_CHUNK - 1) / G4_CHUNK;
@@ -894,9 +903,14 @@ cudaError_t g4_launch_n(G4Params p, cudaStream_t stream) {
 
 template <int XT, int G, bool Z, int MODE>
 cudaError_t g4_launch_p(const G4Params& p, cudaStream_t stream) {
-    // fp32 x: two products a pass (4 columns) where there are that many columns to an expert
-    if constexpr (XT == 1)
-        if (p.R > 2 * (MODE ? p.E : 1)) return g4_launch_n<XT, G, Z, MODE, 2>(p, stream);
+    // fp32 x: two products a pass (4 columns) where there are that many columns to an expert.  Gate/up also where one
+    // column of all of K does not fit beside the rings of 24 warps (G = 32: K above 9984, with zeros 9600; G = 64
+    // with zeros: 12160): those of 16 warps leave room for K = 15488 and more
+    if constexpr (XT == 1) {
+        const int chunks = (p.K + G4_CHUNK - 1) / G4_CHUNK;
+        if (p.R > 2 * (MODE ? p.E : 1) || (MODE == 2 && chunks * g4_x_bytes(G, 2, G4X<XT>::PARTS) > g4_room<G, Z, MODE, 1>()))
+            return g4_launch_n<XT, G, Z, MODE, 2>(p, stream);
+    }
     return g4_launch_n<XT, G, Z, MODE, 1>(p, stream);
 }
 

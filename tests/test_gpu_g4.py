@@ -253,6 +253,35 @@ def test_gate_up(which, N, K, G, zeros, dtype):
     assert (h[lo:] == -5.0).all()
 
 
+@pytest.mark.parametrize("counts", [[0, 1, 0, 2], [3, 0, 9, 1]])      # R below and above 2 E
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("K,G", [(9632, 32), (9984, 32), (10016, 32), (12288, 32), (12160, 64), (12224, 64), (12288, 64),
+                                 (12288, 128)])
+def test_gate_up_of_long_rows(K, G, zeros, dtype, counts):
+    # up to the limit of K, with every type: x of all K is in shared memory, of one column at least
+    N, E, R = 40, len(counts), sum(counts) + 1
+    gate, up = G4(N, K, G, zeros, 11, E=E), G4(N, K, G, zeros, 12, E=E)
+    x = x_of((R, K), dtype, 6, False)
+    h = torch.full((R, N), -5.0, device=DEV)
+    rfx.moe_gate_up_g4(gate.packed, up.packed, gate.stride, N, K, G, x, offsets_of(counts), h, zeros=zeros)
+    # the bound of test_gate_up
+    d = 3 * K * 2.0 ** -23 + (K / G + 17) * 2.0 ** -24
+    lo = 0
+    for e, n in enumerate(counts):
+        if n:
+            xe = x[lo:lo + n].double()
+            g, u = xe @ gate.dense(e).t(), xe @ up.dense(e).t()
+            mg, mu = xe.abs() @ gate.dense(e).abs().t(), xe.abs() @ up.dense(e).abs().t()
+            want = g * torch.sigmoid(g) * u
+            bound = 1.1 * d * mg * u.abs() + d * mu * g.abs() + 1.1 * d * d * mg * mu + 8 * 2.0 ** -23 * want.abs()
+            got = h[lo:lo + n].double()
+            assert bool(((got - want).abs() <= bound + 1e-37).all())
+            assert float((got - want).norm() / want.norm()) <= 1e-5
+        lo += n
+    assert (h[lo:] == -5.0).all()
+
+
 def test_gate_up_far_tail_of_silu():
     # one weight per row picks g and u: silu at the ends of fp32's range of exp
     N, K, G = 16, 32, 32
