@@ -282,6 +282,53 @@ def test_gate_up_of_long_rows(K, G, zeros, dtype, counts):
     assert (h[lo:] == -5.0).all()
 
 
+@pytest.mark.parametrize("counts", [[0, 9, 1, 23], [2, 0, 1, 0, 0, 0, 3, 0]])      # R above and below 2 E
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("K,G,zeros", [(4640, 32, True), (5504, 128, False), (7168, 64, True), (12352, 64, False),
+                                       (14336, 128, True), (14368, 32, True), (30112, 32, False)])
+def test_expert_products_of_long_rows(K, G, zeros, dtype, counts):
+    # x of all K does not fit a CTA's shared memory (8 columns of 16 bits: K above 4224 to 5376; fp32, 2 or 4
+    # columns: 4480 to 7168): K in parts, added in y by one launch after the other, the last part and its last chunk
+    # shorter.  |w x| <= 480 in units of 1/2: integer sums below 2^24 up to K = 34,000
+    N, E, R = 50, len(counts), sum(counts) + 2
+    w = G4(N, K, G, zeros, 23, E=E, integer=True, pad=16)
+    x = x_of((R, K), dtype, 4, True)
+    x[R - 2:] = float("nan")
+    y = torch.full((R, N), -5.0, device=DEV)
+    rfx.moe_gemv_g4(w.packed, w.stride, N, K, G, x, offsets_of(counts), y, zeros=zeros)
+    lo = 0
+    for e, n in enumerate(counts):
+        if n:
+            check(y[lo:lo + n], w.dense(e), x[lo:lo + n], G, integer=True)
+        lo += n
+    assert (y[lo:] == -5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("K,G,zeros", [(4640, 32, True), (5504, 128, False), (7168, 64, True), (9600, 32, False)])
+def test_gate_up_of_long_rows_with_many_of_them(K, G, zeros, dtype):
+    # x of all K leaves room for 4, 2 or 1 columns a pass instead of 8 (fp32: of 4).  Integer inputs, so that the products are
+    # exact: of the size of fp32's whole numbers, so only silu's tail and roundings remain
+    counts, N = [0, 9, 1, 23], 40
+    E, R = len(counts), sum(counts) + 1
+    gate, up = G4(N, K, G, zeros, 31, E=E, integer=True), G4(N, K, G, zeros, 32, E=E, integer=True)
+    x = x_of((R, K), dtype, 4, True)
+    x[R - 1:] = float("nan")
+    h = torch.full((R, N), -5.0, device=DEV)
+    rfx.moe_gate_up_g4(gate.packed, up.packed, gate.stride, N, K, G, x, offsets_of(counts), h, zeros=zeros)
+    lo = 0
+    for e, n in enumerate(counts):
+        if n:
+            xe = x[lo:lo + n].double()
+            g, u = xe @ gate.dense(e).t(), xe @ up.dense(e).t()
+            want = g * torch.sigmoid(g) * u
+            # as in test_expert_products_of_many_passes
+            bound = (6 + 2 * g.abs().clamp(max=104)) * 2.0 ** -23 * want.abs() + 1e-37 * (1 + u.abs())
+            assert bool(((h[lo:lo + n].double() - want).abs() <= bound).all())
+        lo += n
+    assert (h[lo:] == -5.0).all()
+
+
 def test_gate_up_far_tail_of_silu():
     # one weight per row picks g and u: silu at the ends of fp32's range of exp
     N, K, G = 16, 32, 32
