@@ -327,8 +327,8 @@ int rfx_g4_pack_device(const uint8_t* codes, const uint16_t* scales, const uint8
  * magnitude to [2^13, 2^14): bf16 and fp16 values are whole down to 2^-23 of the largest and
  * within 2^-35 of the largest below that; fp32 values enter as three such parts (33 bits).
  * The products code * x are exact; each group's sum, code * x minus zero * sum of x, is taken in
- * fp32, scaled and added in fp32.  The order of the sums depends on N, K and the
- * GPU only (fp32 x: and on q > 2; K in parts: on q), so results repeat bit for bit, whatever the other columns hold.
+ * fp32, scaled and added in fp32.  The order of the sums depends on the matrix (N, K, group, zeros or not), the type
+ * of x and the GPU (fp32 x: and on q > 2; K in parts: on q), so results repeat bit for bit, whatever the other columns hold.
  * A column of x with an infinity or a NaN gives NaN, and no other column does.
  * Limits: 1 <= q <= 8, N >= 1, K % group == 0.  No workspace.  One launch; more where the
  * columns' x does not fit shared memory (about q * K > 45,000 for 16-bit x, 14,000 for fp32) or fp32 x has more than
@@ -348,7 +348,8 @@ int rfx_gemv_g4(const void* W, int64_t N, int64_t K, int group, int has_zeros, c
  * [R][N], rows outside every expert left as they were.  R: rows of x (T * k).
  * A pass over an expert's weights serves up to 8 of its rows (fp32 x: 2, or 4 where R > 2 E);
  * only experts with rows are read.  Meant for decode and verify (few rows an expert).
- * Numerics as rfx_gemv_g4; silu in fp32.  Limits: 1 <= E <= 1024, R >= 0 (R = 0 is a no-op), N >= 1,
+ * Numerics as rfx_gemv_g4; silu in fp32.  The order of a row's sums depends on E and R too, but not on
+ * offsets or on the other rows: between calls of other R the last bits of a row may differ.  Limits: 1 <= E <= 1024, R >= 0 (R = 0 is a no-op), N >= 1,
  * K % group == 0, ceil(N / 16) * R <= 2147483000, and K <= 12288 for moe_gate_up_g4.  No workspace; one launch (moe_gemv_g4:
  * K in parts, a launch each, where x does not fit shared memory).
  */

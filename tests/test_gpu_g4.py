@@ -387,6 +387,35 @@ def test_expert_products_of_many_passes(K, dtype, rows):
     assert bool(((h.double() - want).abs() <= bound).all())
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("E,R,K,G,zeros", [(6, 16, 1024, 64, True), (12, 16, 1024, 64, False), (6, 16, 7168, 32, True)])
+def test_bits_of_a_row_depend_on_no_other_row(E, R, K, G, zeros, dtype):
+    # one row through expert 3, wherever its place and whatever the other experts have: the same bits in every call of
+    # the same E and R (K = 7168: in parts)
+    N = 130
+    w, up = G4(N, K, G, zeros, 41, E=E), G4(N, K, G, zeros, 42, E=E)
+    v = x_of((1, K), dtype, 43, False)[0]
+    first = None
+    for seed, (before, mine, at) in enumerate([(0, 1, 0), (0, R, 7), (5, 3, 2), (9, 2, 0), (1, 9, 8), (R - 1, 1, 0)]):
+        counts = [0] * E
+        counts[3] = mine
+        g = torch.Generator().manual_seed(seed)
+        for e in torch.randint(0, 3, (before,), generator=g).tolist():
+            counts[e] += 1
+        for e in torch.randint(4, E, (R - before - mine,), generator=g).tolist():
+            counts[e] += 1
+        x = x_of((R, K), dtype, 50 + seed, False) * (seed + 1)
+        r = before + at
+        x[r] = v
+        y, h = torch.empty((R, N), device=DEV), torch.empty((R, N), device=DEV)
+        rfx.moe_gemv_g4(w.packed, w.stride, N, K, G, x, offsets_of(counts), y, zeros=zeros)
+        rfx.moe_gate_up_g4(w.packed, up.packed, w.stride, N, K, G, x, offsets_of(counts), h, zeros=zeros)
+        if first is None:
+            first = y[r].clone(), h[r].clone()
+            check(y[r:r + 1], w.dense(3), v[None], G)
+        assert torch.equal(y[r], first[0]) and torch.equal(h[r], first[1])
+
+
 def test_experts_past_4_gib_and_no_rows():
     N, K, G = 48, 256, 64
     w = G4(N, K, G, True, 7, E=3, integer=True)
