@@ -11,10 +11,13 @@
 //   stored divided by 16.
 //   x: brought to max|x| in [2^13, 2^14) by a power of two (per column, over the launch's
 //   part of K) and rounded to fp16.  That keeps bf16 and fp16 values whole down to
-//   2^-23 of the largest, and 2^-35 of the largest below that (fp32 sums keep 2^-24).
+//   2^-23 of the largest, and 2^-34 of the largest below that (fp32 sums keep 2^-24).
 //   fp32 x is cut into three such parts of 11 bits, which are columns of the product.
 //   zero: the sums start from -zero * sum_k x.
-// So the only roundings that count are the fp32 sums and the scale's product.
+// So the only roundings that count are the fp32 sums and the scale's product.  They go with
+// scale (code + zero) |x|, the size of what is summed, not with |W x|: weights near their zero point lose
+// up to 5 bits to that, and a weight of 0 adds a rounding instead of 0.  (code - zero) as operands would
+// not, for 8 more operations per 16 x 32 weights.
 //
 // Why mma.sync and not tcgen05: with 8 columns a 128 x 8 x 16 tcgen05.mma takes as long as one
 // with 128 columns (about 89 cycles, 23 weights a cycle and SM, where the weights arrive at 46),
@@ -544,7 +547,7 @@ __device__ __forceinline__ void g4_stage_x(const G4Params& p, G4Phase& ph, int c
                     s[j & 1] += g.x + g.y;
                     f[2 * j] = (f[2 * j] - g.x) * 2048.f;
                     f[2 * j + 1] = (f[2 * j + 1] - g.y) * 2048.f;
-                } else {   // before rounding: the same but for what the smallest values lose, 2^-35 of the largest
+                } else {   // before rounding: the same but for what the smallest values lose, 2^-34 of the largest
                     s[j & 1] += f[2 * j] + f[2 * j + 1];
                 }
             }

@@ -325,9 +325,12 @@ int rfx_g4_pack_device(const uint8_t* codes, const uint16_t* scales, const uint8
  * aligned.  y: device fp32 [q][N].
  * Numerics: x enters as fp16 after a power of two per column that brings its largest
  * magnitude to [2^13, 2^14): bf16 and fp16 values are whole down to 2^-23 of the largest and
- * within 2^-35 of the largest below that; fp32 values enter as three such parts (33 bits).
+ * within 2^-34 of the largest below that; fp32 values enter as three such parts (33 bits).
  * The products code * x are exact; each group's sum, code * x minus zero * sum of x, is taken in
- * fp32, scaled and added in fp32.  The order of the sums depends on the matrix (N, K, group, zeros or not), the type
+ * fp32, scaled and added in fp32.  The rounding error therefore goes with M = sum scale * (code + zero) * |x|
+ * (zero = 8 without zeros), not with sum |W x|: at most about (G / 16 * 34 + K / G + 51) * 2^-24 * M,
+ * and for 16-bit x 15 * 2^-34 * max |x| * sum scale more.  Weights of exactly 0 (code = zero, as in a pruned
+ * row) add a rounding of that size, not 0, also where their x is an outlier.  The order of the sums depends on the matrix (N, K, group, zeros or not), the type
  * of x and the GPU (fp32 x: and on q > 2; K in parts: on q), so results repeat bit for bit, whatever the other columns hold.
  * A column of x with an infinity or a NaN gives NaN, and no other column does.
  * Limits: 1 <= q <= 8, N >= 1, K % group == 0.  No workspace.  One launch; more where the

@@ -192,6 +192,60 @@ def test_gemv_fp32_x_of_any_size():
     assert bool(((y.double() - want).abs() <= 4 * 2.0 ** -23 * want.abs()).all())
 
 
+def true_bound(w, x, e=0):
+    """The error that the form of the sums allows, in 64 bits.  A group is summed as code * x - zero * sum x, of
+    magnitude S = sum (code + zero) |x|: G / 16 steps of the tensor core with 17 addends, each cut to 24 bits of the
+    largest (17 * G / 16 * 2^-23 S); the sum of x in at most 10 roundings and its product with zero in one; then scaled
+    and added, K / G roundings in a warp and at most 24 + 8 + 8 over warps, CTAs and parts of K.  16-bit values of x far below their
+    column's largest enter within 2^-34 of that, times a code of at most 15."""
+    c = w.codes[e].double().view(w.N, -1, w.G)
+    z = w.z[e].double()[..., None] if w.zeros else 8.0
+    s = w.scales[e].double()[..., None].abs()
+    K, G = w.K, w.G
+    m = x.double().abs() @ ((c + z) * s).view(w.N, K).t()
+    err = (17 * G / 16 * 2.0 ** -23 + (11 + K / G + 40) * 2.0 ** -24) * 1.01 * m
+    if x.dtype is not FF:
+        err = err + 15 * 2.0 ** -34 * x.double().abs().amax(1)[:, None] * (s.sum(1) * G).T
+    return err + 1e-37
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FF])
+@pytest.mark.parametrize("K,G,zeros", [(512, 32, True), (4096, 128, False), (4096, 64, True), (352, 32, False), (20480, 128, True)])
+def test_weights_of_zero_and_near_it(K, G, zeros, dtype):
+    # pruned rows and groups (every code the zero point), rows next to their zero point, outliers of x that
+    # meet weights of 0, and x over the whole range that 16-bit types hold a column's largest and smallest in
+    N = 96
+    w = G4(N, K, G, zeros, 61)
+    z = w.z[0].view(N, -1, 1).expand(N, K // G, G).reshape(N, K) if zeros else torch.full_like(w.codes[0], 8)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(62)
+    c = w.codes[0]
+    c[0:16] = z[0:16]                                                   # pruned rows
+    near = torch.randint(-1, 2, c.shape, generator=g, device=DEV, dtype=torch.int16)
+    c[16:48] = (z[16:48].to(torch.int16) + near[16:48]).clamp(0, 15).to(torch.uint8)
+    c[48:64, K // 2 // G * G:] = z[48:64, K // 2 // G * G:]             # pruned groups
+    far = torch.tensor([3, K // 3, K - 1], device=DEV)
+    c[:80, far] = z[:80, far]                                           # the outliers' weights
+    rfx.rfx_g4_pack_device(c, w.scales[0], w.z[0] if zeros else None, N, K, G, w.packed)
+    W = w.dense()
+    assert bool((W[:16] == 0).all() and (W[:80, far] == 0).all())
+    x = torch.randn((6, K), generator=g, device=DEV)
+    x[1, far] = 3.0e3
+    x[2, far] = 6.0e4
+    x[3] *= torch.exp2(torch.randint(-13, 14, (K,), generator=g, device=DEV).float())
+    x[4] *= torch.exp2(torch.randint(-24, 1, (K,), generator=g, device=DEV).float())
+    x[5] *= 2.0 ** -14
+    x[5, far] = 6.0e4
+    x = x.to(dtype)
+    y = torch.empty((6, N), device=DEV)
+    rfx.rfx_gemv_g4(w.packed, N, K, G, x, y, zeros=zeros)
+    ye = torch.empty((6, N), device=DEV)
+    rfx.moe_gemv_g4(w.packed, w.stride, N, K, G, x, offsets_of([6]), ye, zeros=zeros)
+    want, bound = x.double() @ W.t(), true_bound(w, x)
+    for got in (y, ye):
+        assert bool(((got.double() - want).abs() <= bound).all()), float(((got.double() - want).abs() / bound).max())
+
+
 # ------------------------------------------------------------- experts ---
 
 def offsets_of(counts):
