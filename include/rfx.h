@@ -330,12 +330,15 @@ int rfx_g4_pack_device(const uint8_t* codes, const uint16_t* scales, const uint8
  * fp32, scaled and added in fp32.  The rounding error therefore goes with M = sum scale * (code + zero) * |x|
  * (zero = 8 without zeros), not with sum |W x|: at most about (G / 16 * 34 + K / G + 51) * 2^-24 * M,
  * and for 16-bit x 15 * 2^-34 * max |x| * sum scale more.  Weights of exactly 0 (code = zero, as in a pruned
- * row) add a rounding of that size, not 0, also where their x is an outlier.  The order of the sums depends on the matrix (N, K, group, zeros or not), the type
- * of x and the GPU (fp32 x: and on q > 2; K in parts: on q), so results repeat bit for bit, whatever the other columns hold.
+ * row) add a rounding of that size, not 0, also where their x is an outlier.
+ * The order of the sums depends on the matrix (N, K, group, zeros or not), the type of x and the GPU (fp32 x: and
+ * on q > 2; K in parts: on q), so results repeat bit for bit, whatever the other columns hold.
  * A column of x with an infinity or a NaN gives NaN, and no other column does.
- * Limits: 1 <= q <= 8, N >= 1, K % group == 0.  No workspace.  One launch; more where the
- * columns' x does not fit shared memory (about q * K > 45,000 for 16-bit x, 14,000 for fp32) or fp32 x has more than
- * 4 columns.
+ * Limits: 1 <= q <= 8, N >= 1, K % group == 0.  No workspace.  One launch; two for more than 4 columns of fp32 x
+ * (each reads all weights), and more, of parts of K, where x does not fit shared memory.  A CTA holds, from group 32 with
+ * zeros to group 128 without, K = 4480 to 5632 of 8 columns of 16-bit x, 8192 to 11008 of 4, 20480 to 37632 of one; of fp32
+ * x 4736 to 5504 of 4 columns, 5760 to 7424 of 2, 10240 to 14464 of one.  Where a matrix has few rows, up to 8
+ * CTAs share K and hold as many times that.
  */
 int rfx_gemv_g4(const void* W, int64_t N, int64_t K, int group, int has_zeros, const void* x, rfx_dtype x_dtype, int q,
                 float* y, void* stream);
@@ -349,12 +352,16 @@ int rfx_gemv_g4(const void* W, int64_t N, int64_t K, int group, int has_zeros, c
  * [R][K] of x_dtype, 16-byte aligned; offsets: device int32 [E + 1], ascending, read on the
  * device (values outside [0, R] are taken as the nearer end); y, h: device fp32
  * [R][N], rows outside every expert left as they were.  R: rows of x (T * k).
- * A pass over an expert's weights serves up to 8 of its rows (fp32 x: 2, or 4 where R > 2 E);
- * only experts with rows are read.  Meant for decode and verify (few rows an expert).
+ * A pass over an expert's weights serves up to 8 of its rows (fp32 x: 2, or 4 where R > 2 E); only experts with rows
+ * are read.  Meant for decode and verify (few rows an expert).  moe_gate_up_g4 needs x of all K in a CTA's shared memory,
+ * so a pass serves fewer rows of long K.  From group 32 with zeros to group 128 without, 16-bit x: 8 rows up to
+ * K = 4224 to 5376, 4 up to 7680 to 10496, then 2; fp32 x, R > 2 E: 4 up to 4480 to 5248, 2 up to 8832 to 10496, then 1;
+ * R <= 2 E: 2 up to 5504 to 7168, then 1.
  * Numerics as rfx_gemv_g4; silu in fp32.  The order of a row's sums depends on E and R too, but not on
- * offsets or on the other rows: between calls of other R the last bits of a row may differ.  Limits: 1 <= E <= 1024, R >= 0 (R = 0 is a no-op), N >= 1,
- * K % group == 0, ceil(N / 16) * R <= 2147483000, and K <= 12288 for moe_gate_up_g4.  No workspace; one launch (moe_gemv_g4:
- * K in parts, a launch each, where x does not fit shared memory).
+ * offsets or on the other rows: between calls of other R the last bits of a row may differ.
+ * Limits: 1 <= E <= 1024, R >= 0 (R = 0 is a no-op), N >= 1, K % group == 0, ceil(N / 16) * R <= 2147483000, and
+ * K <= 12288 for moe_gate_up_g4.  No workspace; one launch (moe_gemv_g4: K in parts, a launch each, where x does not fit
+ * shared memory, at the limits of rfx_gemv_g4 less 2 to 7 %).
  */
 int moe_gemv_g4(const void* W, size_t stride, int E, int64_t N, int64_t K, int group, int has_zeros, const void* x,
                 rfx_dtype x_dtype, const int32_t* offsets, int R, float* y, void* stream);
