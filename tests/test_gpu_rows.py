@@ -309,6 +309,54 @@ def test_combine_backward(T, H, k, dtype, out):
     assert torch.equal(dw, dw2) and torch.equal(over[pos[live].long()], dys[pos[live].long()])
 
 
+def shifted(t, off):
+    """A copy of t that begins `off` elements past a 16-byte boundary, and the buffer it lies in."""
+    raw = torch.full((t.numel() + off + 16,), 3.0, dtype=t.dtype, device=DEV)
+    v = raw[off:off + t.numel()].view(t.shape)
+    v.copy_(t)
+    assert v.data_ptr() == raw.data_ptr() + off * t.element_size()
+    return v, raw
+
+
+def untouched(v, raw, off):
+    return bool((raw[:off] == 3.0).all() and (raw[off + v.numel():] == 3.0).all())
+
+
+# elements that ys (or dxs), the token side (base, y, dy, dx) and dys lie off a 16-byte boundary: pieces of 16 bytes,
+# of two elements and of one
+OFFS = [(0, 0, 0), (0, 2, 0), (2, 0, 2), (4, 4, 4), (1, 0, 0), (0, 1, 0), (0, 0, 1), (2, 2, 3), (3, 5, 7)]
+
+
+@pytest.mark.parametrize("ro,to,do", OFFS)
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (HF, FF), (FF, FF)])
+def test_combine_and_gradients_at_any_element_alignment(dtype, out, ro, to, do):
+    T, H, k = 21, 264, 5
+    ys, pos, w, b = random_case(T, H, k, dtype, out, 31, base=True)
+    ys, _ = shifted(ys, ro)
+    b, _ = shifted(b, to)
+    y, yraw = shifted(torch.full((T, H), float("nan"), dtype=out, device=DEV), to)
+    rfx.moe_combine_rows(ys, pos, w, y, base=b)
+    check_sum(y, *combine64(ys, pos, w, b), terms=k + 1)
+    assert untouched(y, yraw, to)
+    dx, dxraw = shifted(torch.full((T, H), float("nan"), dtype=dtype, device=DEV), to)
+    rfx.moe_group_tokens_backward(ys, pos, dx)
+    check_sum(dx, *combine64(ys, pos, None, None), terms=k)
+    assert untouched(dx, dxraw, to)
+    # the gradients: the same bits for dys as without the shift, dw's sums in another order
+    dy = torch.randn((T, H), device=DEV).to(out)
+    want, dw = torch.full_like(ys, 5.0), torch.empty_like(w)
+    rfx.moe_combine_rows_backward(dy, ys.clone(), pos, w, want, dw)
+    dys, dysraw = shifted(torch.full_like(ys, 5.0), do)
+    dw2 = torch.full_like(w, float("nan"))
+    rfx.moe_combine_rows_backward(shifted(dy, to)[0], ys, pos, w, dys, dw2)
+    assert torch.equal(dys, want) and untouched(dys, dysraw, do)
+    live = pos >= 0
+    rows = torch.where(live[..., None], ys.double()[pos.clamp(min=0).long()], torch.zeros((), dtype=torch.float64, device=DEV))
+    terms = dy.double()[:, None, :] * rows
+    assert bool(((dw2.double() - terms.sum(2)).abs() <= H * U * terms.abs().sum(2) + 1e-38).all())
+    assert (dw2[~live] == 0).all()
+
+
 def test_combine_gradients_against_differences():
     # L = <c, combine(ys, w)> is linear in ys and in w: its difference quotient is exact up to rounding
     T, H, k = 5, 96, 3
