@@ -19,7 +19,7 @@ struct G4Params {
     int c0, c1;               // chunks of this launch; c0 > 0 adds to y
     int units;                // units of a matrix
     int team, teams, inv_team;   // warps that share a unit, such teams in a CTA, 65536 / team
-    int split;                // CTAs of a cluster that share a unit's K (a power of two)
+    int split;                // CTAs of a cluster that share a unit's K (1 to 8)
     int cols, shift;          // rows of x per pass over a matrix, at most (experts: 1 << shift)
     int x_room;               // shared memory for x
 };
