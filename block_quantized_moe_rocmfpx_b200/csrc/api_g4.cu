@@ -30,6 +30,9 @@ bool shape_ok(int64_t rows, int64_t cols, int G) {
     return group_ok(G) && rows >= 0 && rows <= 2147483647LL && cols > 0 && cols % G == 0 && cols <= 1073741824LL;
 }
 
+// units of 32 rows are counted in 32 bits, the rows behind the last included
+constexpr int64_t kMaxN = 2147483647LL - 31;
+
 const char* const kShape = ": need group 32, 64 or 128, 0 <= rows < 2^31 and cols a positive multiple of group, <= 2^30";
 
 int launch(const rfx::G4Params& p, int dtype, int G, bool zeros, void* stream, const char* who) {
@@ -44,6 +47,7 @@ int experts(const char* who, const void* W0, const void* W1, bool pair, size_t s
     if (!shape_ok(N, K, G) || N < 1) return rfx_fail(RFX_EINVAL, std::string(who) + kShape + " (and N >= 1)");
     if (x_dtype != RFX_BF16 && x_dtype != RFX_F32 && x_dtype != RFX_F16)
         return rfx_fail(RFX_EINVAL, std::string(who) + ": bad x_dtype");
+    if (N > kMaxN) return rfx_fail(RFX_EUNSUPPORTED, std::string(who) + ": N <= 2^31 - 32");
     if (E < 1 || E > 1024 || R < 0) return rfx_fail(RFX_EINVAL, std::string(who) + ": need 1 <= E <= 1024 and R >= 0");
     if (pair && K > 12288) return rfx_fail(RFX_EUNSUPPORTED, std::string(who) + ": K <= 12288");
     if ((N + 15) / 16 * R > 2147483000LL)   // units are counted in 32 bits, a team's step past the last included
@@ -114,6 +118,7 @@ extern "C" int rfx_gemv_g4(const void* W, int64_t N, int64_t K, int group, int h
     if (!shape_ok(N, K, group) || N < 1) return rfx_fail(RFX_EINVAL, std::string("rfx_gemv_g4") + kShape + " (and N >= 1)");
     if (x_dtype != RFX_BF16 && x_dtype != RFX_F32 && x_dtype != RFX_F16)
         return rfx_fail(RFX_EINVAL, "rfx_gemv_g4: bad x_dtype");
+    if (N > kMaxN) return rfx_fail(RFX_EUNSUPPORTED, "rfx_gemv_g4: N <= 2^31 - 32");
     if (q < 1 || q > 8) return rfx_fail(RFX_EUNSUPPORTED, "rfx_gemv_g4: 1 <= q <= 8");
     if (!W || !x || !y) return rfx_fail(RFX_EINVAL, "rfx_gemv_g4: null pointer");
     if (!aligned16(W) || !aligned16(x)) return rfx_fail(RFX_EINVAL, "rfx_gemv_g4: W and x must be 16-byte aligned");

@@ -334,7 +334,7 @@ int rfx_g4_pack_device(const uint8_t* codes, const uint16_t* scales, const uint8
  * The order of the sums depends on the matrix (N, K, group, zeros or not), the type of x and the GPU (fp32 x: and
  * on q > 2; K in parts: on q), so results repeat bit for bit, whatever the other columns hold.
  * A column of x with an infinity or a NaN gives NaN, and no other column does.
- * Limits: 1 <= q <= 8, N >= 1, K % group == 0.  No workspace.  One launch; two for more than 4 columns of fp32 x
+ * Limits: 1 <= q <= 8, 1 <= N <= 2^31 - 32, K % group == 0.  No workspace.  One launch; two for more than 4 columns of fp32 x
  * (each reads all weights), and more, of parts of K, where x does not fit shared memory.  A CTA holds, from group 32 with
  * zeros to group 128 without, K = 4480 to 5632 of 8 columns of 16-bit x, 8192 to 11008 of 4, 20480 to 37632 of one; of fp32
  * x 4736 to 5504 of 4 columns, 5760 to 7424 of 2, 10240 to 14464 of one.  Where a matrix has few rows, up to 8
@@ -359,7 +359,7 @@ int rfx_gemv_g4(const void* W, int64_t N, int64_t K, int group, int has_zeros, c
  * R <= 2 E: 2 up to 5504 to 7168, then 1.
  * Numerics as rfx_gemv_g4; silu in fp32.  The order of a row's sums depends on E and R too, but not on
  * offsets or on the other rows: between calls of other R the last bits of a row may differ.
- * Limits: 1 <= E <= 1024, R >= 0 (R = 0 is a no-op), N >= 1, K % group == 0, ceil(N / 16) * R <= 2147483000, and
+ * Limits: 1 <= E <= 1024, R >= 0 (R = 0 is a no-op), 1 <= N <= 2^31 - 32, K % group == 0, ceil(N / 16) * R <= 2147483000, and
  * K <= 12288 for moe_gate_up_g4.  No workspace; one launch (moe_gemv_g4: K in parts, a launch each, where x does not fit
  * shared memory, at the limits of rfx_gemv_g4 less 2 to 7 %).
  */

@@ -136,6 +136,16 @@ def test_expert_product_refusals():
     assert plain(N=2 ** 20, st=rfx.rfx_g4_packed_bytes(2 ** 20, 256, 64), R=2 ** 15) == rfx.RFX_EUNSUPPORTED
 
 
+@pytest.mark.parametrize("N", [2 ** 31 - 31, 2 ** 31 - 1])
+def test_products_refuse_rows_that_do_not_fit_32_bits(N):
+    # units of 32 rows are counted in 32 bits, the rows behind the last included
+    assert rfx.rfx_g4_packed_bytes(N, 32, 32) > 0
+    assert rfx._gemv_g4(A, N, 32, 32, 0, A, 0, 1, A, None) == rfx.RFX_EUNSUPPORTED
+    n = rfx.rfx_g4_packed_bytes(N, 32, 32)
+    assert rfx._moe_g4(A, n, 1, N, 32, 32, 0, A, 0, A, 1, A, None) == rfx.RFX_EUNSUPPORTED
+    assert rfx._moe_gate_up_g4(A, A, n, 1, N, 32, 32, 0, A, 0, A, 1, A, None) == rfx.RFX_EUNSUPPORTED
+
+
 def test_device_pack_refusals():
     def call(c=A, s=A, z=None, rows=16, cols=64, G=64, dst=A):
         return rfx._g4_pack_device(c, s, z, rows, cols, G, dst, None)
