@@ -24,6 +24,7 @@ int cuda_fail(const char* where, cudaError_t e) {
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 bool group_ok(int G) { return G == 32 || G == 64 || G == 128; }
 // rows and columns whose packed size and indexes stay far below 2^63
 bool shape_ok(int64_t rows, int64_t cols, int G) {
@@ -56,6 +57,8 @@ int experts(const char* who, const void* W0, const void* W1, bool pair, size_t s
     if (!W0 || (pair && !W1) || !x || !offsets || !y) return rfx_fail(RFX_EINVAL, std::string(who) + ": null pointer");
     if (!aligned16(W0) || !aligned16(W1) || stride % 16 || !aligned16(x))
         return rfx_fail(RFX_EINVAL, std::string(who) + ": weights, stride and x must be 16-byte aligned");
+    if (!aligned4(offsets) || !aligned4(y))
+        return rfx_fail(RFX_EINVAL, std::string(who) + ": offsets and the output must be 4-byte aligned");
     if (E > 1 && stride < rfx_g4_packed_bytes(N, K, G, has_zeros))
         return rfx_fail(RFX_EINVAL, std::string(who) + ": stride smaller than the packed matrix");
     rfx::G4Params p = {};
@@ -122,6 +125,7 @@ extern "C" int rfx_gemv_g4(const void* W, int64_t N, int64_t K, int group, int h
     if (q < 1 || q > 8) return rfx_fail(RFX_EUNSUPPORTED, "rfx_gemv_g4: 1 <= q <= 8");
     if (!W || !x || !y) return rfx_fail(RFX_EINVAL, "rfx_gemv_g4: null pointer");
     if (!aligned16(W) || !aligned16(x)) return rfx_fail(RFX_EINVAL, "rfx_gemv_g4: W and x must be 16-byte aligned");
+    if (!aligned4(y)) return rfx_fail(RFX_EINVAL, "rfx_gemv_g4: y must be 4-byte aligned");
     rfx::G4Params p = {};
     p.W0 = (const uint8_t*)W;
     p.E = 1; p.R = q; p.N = (int)N; p.K = (int)K;

@@ -19,6 +19,8 @@ int cuda_fail(const char* where, cudaError_t e) {
 bool dtype_ok(int d) { return d == RFX_BF16 || d == RFX_F32 || d == RFX_F16; }
 size_t dtype_bytes(int d) { return d == RFX_F32 ? 4 : 2; }
 bool aligned_to(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+template <typename... P>
+bool aligned4(const P*... p) { return ((((uintptr_t)p & 3u) == 0) && ...); }
 
 // Shared limits of the row calls; RFX_OK or the error.
 int check_rows(const char* who, int dtype, int T, int H, int k) {
@@ -51,6 +53,8 @@ extern "C" int moe_group_tokens(const void* x, rfx_dtype dtype, int T, int H, co
         return rfx_fail(RFX_EINVAL, "moe_group_tokens: null pointer (x and xs may both be null)");
     if (!aligned_to(x, dtype_bytes(dtype)) || !aligned_to(xs, dtype_bytes(dtype)))
         return rfx_fail(RFX_EINVAL, "moe_group_tokens: x and xs must be aligned to their element");
+    if (!aligned4(idx, pos, rows, offsets))
+        return rfx_fail(RFX_EINVAL, "moe_group_tokens: idx, pos, rows and offsets must be 4-byte aligned");
     if (!aligned_to(ws, 256)) return rfx_fail(RFX_EINVAL, "moe_group_tokens: ws must be 256-byte aligned");
     if (ws_bytes < moe_group_workspace_bytes(T, k, E))
         return rfx_fail(RFX_EINVAL, "moe_group_tokens: workspace smaller than moe_group_workspace_bytes");
@@ -75,6 +79,7 @@ extern "C" int moe_group_tokens_backward(const void* dxs, rfx_dtype dtype, int T
     if (!dxs || !pos || !dx) return rfx_fail(RFX_EINVAL, "moe_group_tokens_backward: null pointer");
     if (!aligned_to(dxs, dtype_bytes(dtype)) || !aligned_to(dx, dtype_bytes(dtype)))
         return rfx_fail(RFX_EINVAL, "moe_group_tokens_backward: dxs and dx must be aligned to their element");
+    if (!aligned4(pos)) return rfx_fail(RFX_EINVAL, "moe_group_tokens_backward: pos must be 4-byte aligned");
     cudaError_t e = rfx::combine_launch(dxs, dtype, T, H, pos, k, nullptr, nullptr, dx, dtype, (cudaStream_t)stream);
     return e == cudaSuccess ? RFX_OK : cuda_fail("moe_group_tokens_backward", e);
 }
@@ -90,6 +95,7 @@ extern "C" int moe_combine_rows(const void* ys, rfx_dtype dtype, int T, int H, c
     if (!aligned_to(ys, dtype_bytes(dtype)) || !aligned_to(y, dtype_bytes(y_dtype)) ||
         !aligned_to(base, dtype_bytes(y_dtype)))
         return rfx_fail(RFX_EINVAL, "moe_combine_rows: ys, base and y must be aligned to their element");
+    if (!aligned4(pos, w)) return rfx_fail(RFX_EINVAL, "moe_combine_rows: pos and w must be 4-byte aligned");
     cudaError_t e = rfx::combine_launch(ys, dtype, T, H, pos, k, w, base, y, y_dtype, (cudaStream_t)stream);
     return e == cudaSuccess ? RFX_OK : cuda_fail("moe_combine_rows", e);
 }
@@ -107,6 +113,7 @@ extern "C" int moe_combine_rows_backward(const void* dy, rfx_dtype y_dtype, cons
     if (!aligned_to(ys, dtype_bytes(dtype)) || !aligned_to(dys, dtype_bytes(dtype)) ||
         !aligned_to(dy, dtype_bytes(y_dtype)))
         return rfx_fail(RFX_EINVAL, "moe_combine_rows_backward: dy, ys and dys must be aligned to their element");
+    if (!aligned4(pos, w, dw)) return rfx_fail(RFX_EINVAL, "moe_combine_rows_backward: pos, w and dw must be 4-byte aligned");
     cudaError_t e = rfx::combine_backward_launch(dy, y_dtype, ys, dtype, T, H, pos, k, w, dys, dw, (cudaStream_t)stream);
     return e == cudaSuccess ? RFX_OK : cuda_fail("moe_combine_rows_backward", e);
 }
@@ -117,6 +124,8 @@ extern "C" int moe_router_topk_backward(const int32_t* idx, const float* w, cons
         return rfx_fail(RFX_EINVAL, "moe_router_topk_backward: need T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 16)");
     if (T == 0) return RFX_OK;
     if (!idx || !w || !dw || !dlogits) return rfx_fail(RFX_EINVAL, "moe_router_topk_backward: null pointer");
+    if (!aligned4(idx, w, dw, dlogits))
+        return rfx_fail(RFX_EINVAL, "moe_router_topk_backward: idx, w, dw and dlogits must be 4-byte aligned");
     cudaError_t e = rfx::router_backward_launch(idx, w, dw, T, E, k, dlogits, (cudaStream_t)stream);
     return e == cudaSuccess ? RFX_OK : cuda_fail("moe_router_topk_backward", e);
 }

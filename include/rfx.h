@@ -31,7 +31,8 @@
  *    "host" pointers are CPU memory.  All buffers are owned by the caller; the
  *    library never allocates device memory (moe_layer_create allocates only a
  *    small host struct; moe_ffn_forward_static uses a workspace array compiled
- *    into the library).
+ *    into the library).  A pointer is aligned to its element (int32 and fp32: 4
+ *    bytes) where a call asks no more.
  *  - Device calls are asynchronous on `stream` (a cudaStream_t, NULL = legacy
  *    default stream).  The return code covers argument validation and launch
  *    errors.  Errors found on the device (expert id out of range, a SwiGLU

@@ -146,6 +146,15 @@ def test_products_refuse_rows_that_do_not_fit_32_bits(N):
     assert rfx._moe_gate_up_g4(A, A, n, 1, N, 32, 32, 0, A, 0, A, 1, A, None) == rfx.RFX_EUNSUPPORTED
 
 
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_offsets_and_outputs_must_be_aligned_to_4_bytes(off):
+    n, B = rfx.rfx_g4_packed_bytes(64, 256, 64), A + off
+    assert rfx._gemv_g4(A, 64, 256, 64, 0, A, 0, 1, B, None) == rfx.RFX_EINVAL
+    for offsets, y in ((B, A), (A, B)):
+        assert rfx._moe_g4(A, n, 4, 64, 256, 64, 0, A, 0, offsets, 3, y, None) == rfx.RFX_EINVAL
+        assert rfx._moe_gate_up_g4(A, A, n, 4, 64, 256, 64, 0, A, 0, offsets, 3, y, None) == rfx.RFX_EINVAL
+
+
 def test_device_pack_refusals():
     def call(c=A, s=A, z=None, rows=16, cols=64, G=64, dst=A):
         return rfx._g4_pack_device(c, s, z, rows, cols, G, dst, None)

@@ -75,6 +75,24 @@ def test_router_backward_refusals():
     assert call(T=0, dl=None) == rfx.RFX_OK
 
 
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_indexes_and_weights_must_be_aligned_to_4_bytes(off):
+    E, B = rfx.RFX_EINVAL, A + off
+    for name in ("idx", "pos", "rows", "off"):
+        assert group(**{name: B}) == E, name
+    assert code(rfx._group_bwd(A, 0, 4, 8, B, 2, A, None)) == E
+    assert code(rfx._combine(A, 0, 4, 8, B, 2, A, None, A, 1, None)) == E
+    assert code(rfx._combine(A, 0, 4, 8, A, 2, B, None, A, 1, None)) == E
+    for at in (6, 8, 10):       # pos, w, dw
+        args = [A, 1, A, 0, 4, 8, A, 2, A, A, A, None]
+        args[at] = B
+        assert code(rfx._combine_bwd(*args)) == E, at
+    for at in (0, 1, 2, 6):     # idx, w, dw, dlogits
+        args = [A, A, A, 4, 8, 2, A, None]
+        args[at] = B
+        assert code(rfx._router_bwd(*args)) == E, at
+
+
 def test_python_refuses_host_tensors():
     t = torch.zeros((2, 2))
     with pytest.raises(ValueError):
