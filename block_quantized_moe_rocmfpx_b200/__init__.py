@@ -383,18 +383,28 @@ def rfx_g4_packed_bytes(rows: int, cols: int, group: int, zeros: bool = False) -
     return int(_g4_bytes(rows, cols, group, 1 if zeros else 0))
 
 
+def _whole(name: str, a, dtype) -> np.ndarray:
+    """A contiguous array of whole numbers as dtype; refused where a cast would change a value."""
+    a = np.ascontiguousarray(a)
+    if a.dtype == dtype:
+        return a
+    if a.dtype.kind not in "iu" or (a.size and (a.min() < 0 or a.max() > np.iinfo(dtype).max)):
+        raise ValueError(f"{name}: whole numbers from 0 to {np.iinfo(dtype).max} expected (dtype {a.dtype})")
+    return a.astype(dtype)
+
+
 def rfx_g4_pack(codes: np.ndarray, scales: np.ndarray, group: int, zeros: np.ndarray | None = None) -> np.ndarray:
     """codes uint8 [rows][cols] (< 16), scales binary16 (float16 or its bits) and zeros
     uint8 (< 16) or None, both [rows][cols/group] -> packed bytes (host)."""
-    codes = np.ascontiguousarray(codes, dtype=np.uint8)
+    codes = _whole("codes", codes, np.uint8)
     rows, cols = codes.shape
     scales = np.ascontiguousarray(scales)
-    scales = scales.view(np.uint16) if scales.dtype == np.float16 else np.ascontiguousarray(scales, dtype=np.uint16)
+    scales = scales.view(np.uint16) if scales.dtype in (np.float16, np.int16) else _whole("scales", scales, np.uint16)
     nbytes = rfx_g4_packed_bytes(rows, cols, group, zeros is not None)
     if nbytes and scales.shape != (rows, cols // group):
         raise ValueError(f"scales: shape {scales.shape}, expected {(rows, cols // group)}")
     if zeros is not None:
-        zeros = np.ascontiguousarray(zeros, dtype=np.uint8)
+        zeros = _whole("zeros", zeros, np.uint8)
         if zeros.shape != scales.shape:
             raise ValueError(f"zeros: shape {zeros.shape}, expected {scales.shape}")
     out = np.empty(nbytes, dtype=np.uint8)

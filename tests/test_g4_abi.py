@@ -105,6 +105,21 @@ def test_pack_refuses_bad_values():
         rfx.rfx_g4_unpack(np.zeros(10, np.uint8), 16, 64, 32)
 
 
+def test_python_pack_refuses_arrays_that_a_cast_would_change():
+    c, s, z = weights(16, 64, 32, True)
+    want = rfx.rfx_g4_pack(c, s, 32, z)
+    # other integer types that hold the same values, and the scales' bits as such
+    assert np.array_equal(rfx.rfx_g4_pack(c.astype(np.int64), s.view(np.uint16), 32, z.astype(np.int32)), want)
+    assert np.array_equal(rfx.rfx_g4_pack(c.tolist(), s.view(np.int16), 32, z.tolist()), want)
+    big = c.astype(np.int64)
+    big[2, 3] = 256 + 5
+    for bad in ((big, s, z), (c - np.int64(300), s, z), (c, s, z.astype(np.int64) + 256), (c.astype(np.float32), s, z),
+                (c, s, z.astype(np.float64)), (c, s.astype(np.float32), z), (c, s.astype(np.float64), z),
+                (c, s.view(np.uint16).astype(np.int64) + 65536, z)):
+        with pytest.raises(ValueError):
+            rfx.rfx_g4_pack(bad[0], bad[1], 32, bad[2])
+
+
 def test_gemv_refusals():
     def call(W=A, N=64, K=256, G=64, z=0, x=A, dt=0, q=1, y=A):
         return rfx._gemv_g4(W, N, K, G, z, x, dt, q, y, None)
