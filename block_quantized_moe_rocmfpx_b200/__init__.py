@@ -250,6 +250,13 @@ def _dense(name: str, t, dev: int, shape, dtype=None):
     raise ValueError(f"{name}: must be contiguous")
 
 
+_I32_MAX = 2147483647   # ctypes cuts larger sizes to 32 bits
+
+
+def _too_large(*sizes):
+    raise ValueError(f"sizes {sizes}: each must be below 2^31")
+
+
 def _bytes_at_least(name: str, t, dev: int, n: int):
     if t.get_device() != dev:
         raise ValueError(f"{name}: must be on the current CUDA device, not {t.device}")
@@ -277,6 +284,8 @@ def moe_router_topk_backward(idx, w, dw, dlogits, stream=None):
     dev = _on("dlogits", dlogits)
     T, E = dlogits.shape
     k = idx.shape[-1]
+    if T > _I32_MAX or k > _I32_MAX or E > _I32_MAX:
+        _too_large(T, k, E)
     rt, tk = _RT, (T, k)
     _dense("dlogits", dlogits, dev, (T, E), rt.f32)
     _dense("idx", idx, dev, tk, rt.i32)
@@ -312,6 +321,8 @@ def moe_group_tokens(x, idx, E: int, xs, pos, rows, offsets, ws, stream=None):
         _dense("x", x, dev, (T, H))
         _dense("xs", xs, dev, (T * k, H), x.dtype)
         px, pxs = x.data_ptr(), xs.data_ptr()
+    if T > _I32_MAX or k > _I32_MAX or E > _I32_MAX or H > _I32_MAX:
+        _too_large(T, k, E, H)
     rc = _group(px, dt, T, H, idx.data_ptr(), k, E, pxs, pos.data_ptr(), rows.data_ptr(), offsets.data_ptr(),
                 ws.data_ptr(), ws.numel() * ws.element_size(), _on_stream(stream, dev))
     if rc:
@@ -323,6 +334,8 @@ def moe_group_tokens_backward(dxs, pos, dx, stream=None):
     dev = _on("pos", pos)
     T, k = pos.shape
     H = dx.shape[-1]
+    if T > _I32_MAX or k > _I32_MAX or H > _I32_MAX:
+        _too_large(T, k, H)
     _dense("pos", pos, dev, (T, k), _RT.i32)
     _dense("dxs", dxs, dev, (T * k, H), dx.dtype)
     _dense("dx", dx, dev, (T, H))
@@ -338,6 +351,8 @@ def moe_combine_rows(ys, pos, w, y, base=None, stream=None):
     dev = _on("pos", pos)
     T, k = pos.shape
     H = y.shape[-1]
+    if T > _I32_MAX or k > _I32_MAX or H > _I32_MAX:
+        _too_large(T, k, H)
     _dense("pos", pos, dev, (T, k), _RT.i32)
     _dense("w", w, dev, (T, k), _RT.f32)
     _dense("ys", ys, dev, (T * k, H))
@@ -357,6 +372,8 @@ def moe_combine_rows_backward(dy, ys, pos, w, dys, dw, stream=None):
     dev = _on("pos", pos)
     T, k = pos.shape
     H = dy.shape[-1]
+    if T > _I32_MAX or k > _I32_MAX or H > _I32_MAX:
+        _too_large(T, k, H)
     _dense("pos", pos, dev, (T, k), _RT.i32)
     _dense("w", w, dev, (T, k), _RT.f32)
     _dense("ys", ys, dev, (T * k, H))

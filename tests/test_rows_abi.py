@@ -101,6 +101,60 @@ def test_python_refuses_host_tensors():
         rfx.moe_combine_rows(torch.zeros((4, 8)), t.int(), t, torch.zeros((2, 8)))
 
 
+class Fake:
+    """What the binding sees of a device tensor, of any size."""
+
+    def __init__(self, *shape, dtype=torch.float32):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, "cuda:0"
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return A
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return 4
+
+
+@pytest.mark.parametrize("T,H", [(2 ** 32, 8), (2 ** 32 + 5, 1), (2 ** 31, 1), (1, 2 ** 32 + 8)])
+def test_python_refuses_sizes_that_do_not_fit_the_call(T, H, monkeypatch):
+    class Runtime:
+        i32, f32, codes = torch.int32, torch.float32, {torch.float32: rfx.RFX_F32}
+        device, stream = staticmethod(lambda: 0), staticmethod(lambda dev: 0)
+
+    monkeypatch.setattr(rfx, "_RT", Runtime)
+    for name in ("_group", "_group_bwd", "_combine", "_combine_bwd", "_router_bwd"):
+        monkeypatch.setattr(rfx, name, lambda *args: pytest.fail("the sizes reached the call cut to 32 bits"))
+    i = Fake(T, 1, dtype=torch.int32)
+    w, x, xs, off = Fake(T, 1), Fake(T, H), Fake(T, H), Fake(9, dtype=torch.int32)
+    for call in (lambda: rfx.moe_group_tokens(x, i, 8, xs, i, Fake(T, dtype=torch.int32), off, Fake(1 << 20)),
+                 lambda: rfx.moe_group_tokens_backward(xs, i, x), lambda: rfx.moe_combine_rows(xs, i, w, x),
+                 lambda: rfx.moe_combine_rows_backward(x, xs, i, w, xs, w)):
+        with pytest.raises(ValueError):
+            call()
+    many = 2 ** 32 + 2       # experts, or entries of a token
+    one, ids, w1 = Fake(1, H), Fake(1, many, dtype=torch.int32), Fake(1, many)
+    for call in (lambda: rfx.moe_router_topk_backward(Fake(1, 2, dtype=torch.int32), Fake(1, 2), Fake(1, 2), w1),
+                 lambda: rfx.moe_router_topk_backward(ids, w1, w1, Fake(1, 8)),
+                 lambda: rfx.moe_combine_rows(Fake(many, H), ids, w1, one),
+                 lambda: rfx.moe_group_tokens(None, Fake(1, 2, dtype=torch.int32), many, None, Fake(1, 2, dtype=torch.int32),
+                                              Fake(2, dtype=torch.int32), Fake(many + 1, dtype=torch.int32), Fake(1 << 20))):
+        with pytest.raises(ValueError):
+            call()
+    if H == 1:
+        with pytest.raises(ValueError):
+            rfx.moe_router_topk_backward(i, w, w, Fake(T, 1))
+        with pytest.raises(ValueError):
+            rfx.moe_group_tokens(None, i, 8, None, i, Fake(T, dtype=torch.int32), off, Fake(1 << 20))
+
+
 def test_dtype_codes_match_the_header():
     assert (rfx.RFX_BF16, rfx.RFX_F32, rfx.RFX_F16) == (0, 1, 2)
     assert ctypes.sizeof(ctypes.c_int) == 4
