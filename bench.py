@@ -59,7 +59,7 @@ TRAFFIC = {
     ("moe_decode", "q1"): ("557fce27bf9ab819", 67_082_240 + 866_816, 66_872_368),
     ("moe_decode", "q4"): ("557fce27bf9ab819", 111_705_856 + 3_130_368, 111_513_792),
     # both pf_gemm launches of one T = 2048 step (gate/up + down), token batch 0
-    ("prefill", "T2048"): ("ab522f207f7dd16d", 751_524_096 + 42_337_024 + 522_533_120 + 3_903_232, 1_070_858_240),
+    ("prefill", "T2048"): ("dae1fd17a1b7c4b8", 752_586_496 + 41_641_472 + 521_991_680 + 3_984_640, 1_070_858_240),
 }
 
 
