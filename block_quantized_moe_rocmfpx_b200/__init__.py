@@ -661,7 +661,8 @@ class MoeLayer:
         # mix: ROCmFPX MIX table, E tuples (f_gate_up, f_down, off_gate, off_up, off_down)
         self.handle = moe_layer_create(d) if mix is None else moe_layer_create_mix(d, mix)
         self.max_T = max_T
-        nbytes = moe_ffn_workspace_bytes(self.handle, max_T)
+        # of a call of any T up to max_T: a short prefill's may be smaller than decode's
+        nbytes = max(moe_ffn_workspace_bytes(self.handle, max_T), moe_ffn_workspace_bytes(self.handle, min(max_T, 8)))
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=gate.device)
         rfx_ws_init(self.ws)
 

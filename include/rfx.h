@@ -421,7 +421,7 @@ int moe_layer_create_mix(const moe_layer_desc* d, const moe_expert_mix* mix, moe
 
 /*
  * Device workspace bytes moe_ffn_forward needs for T token columns (T > 8:
- * the prefill workspace, moe_prefill_workspace_bytes).  The
+ * the prefill workspace, moe_prefill_workspace_bytes, for few tokens less than that of T = 8).  The
  * workspace holds counters, the SwiGLU intermediate and per-expert partial
  * outputs; it must be zeroed once (rfx_ws_init) before its first use and may
  * then be reused by successive calls on the same stream, of any T that it is

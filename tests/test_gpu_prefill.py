@@ -256,6 +256,28 @@ def test_decode_after_prefill_on_one_workspace(exact):
     assert rfx.rfx_ws_status(ws) == rfx.RFX_OK
 
 
+def test_a_layer_takes_every_T_up_to_its_largest():
+    # the prefill workspace of a few tokens is smaller than decode's of 8
+    H, I, E, k = 512, 256, 8, 2
+    lay = SynthLayer(58, 0, H, I, E, k)
+    ml = lay.moe_layer(max_T=9)
+    ref = lay.moe_layer()
+    for T in (9, 8, 5, 9, 1):
+        idx = torch.empty((T, k), dtype=torch.int32, device=DEV)
+        w = torch.empty((T, k), dtype=torch.float32, device=DEV)
+        rfx.moe_router_topk(to_dev(synth.logits(58, 0, T, T, E, 0.0)), k, idx, w)
+        x = to_dev(synth.x_bf16(58, T, T, H), torch.bfloat16)
+        y, want = (torch.empty((T, H), device=DEV) for _ in range(2))
+        ml.forward(x, idx, w, y)
+        if T <= 8:
+            ref.forward(x, idx, w, want)
+            assert torch.equal(y, want), T
+        else:
+            ref.prefill(x, idx, w, want)
+            torch.testing.assert_close(y, want, rtol=1e-6, atol=1e-6 * float(want.abs().max()))
+    assert ml.status() == rfx.RFX_OK
+
+
 def test_prefill_bad_expert_ids_set_the_device_flag():
     lay = SynthLayer(59, 0, 512, 256, 8, 2)
     ml = lay.moe_layer()
