@@ -661,10 +661,27 @@ class MoeLayer:
         # mix: ROCmFPX MIX table, E tuples (f_gate_up, f_down, off_gate, off_up, off_down)
         self.handle = moe_layer_create(d) if mix is None else moe_layer_create_mix(d, mix)
         self.max_T = max_T
+        self._used_on = {}   # streams that a kept workspace was used on
         # of a call of any T up to max_T: a short prefill's may be smaller than decode's
         nbytes = max(moe_ffn_workspace_bytes(self.handle, max_T), moe_ffn_workspace_bytes(self.handle, min(max_T, 8)))
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=gate.device)
         rfx_ws_init(self.ws)
+
+    def _kept(self, name: str, nbytes: int, stream: int):
+        """The workspace kept as `name`, grown to nbytes, for a call on `stream`: its memory comes from that
+        stream and is zeroed there, and goes back when every stream that used it is through."""
+        import torch
+        ws = getattr(self, name, None)
+        if ws is None or ws.numel() < nbytes:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.ws.device)):
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=self.ws.device)
+            rfx_ws_init(ws, stream)
+            setattr(self, name, ws)
+            self._used_on[name] = {stream}
+        elif stream not in self._used_on[name]:
+            ws.record_stream(torch.cuda.ExternalStream(stream, device=ws.device))
+            self._used_on[name].add(stream)
+        return ws
 
     def forward(self, x, idx, w, y, stream=None):
         T = x.shape[0]
@@ -682,15 +699,12 @@ class MoeLayer:
     def forward_host(self, x, logits, y, stream=None):
         """Router + FFN from host buffers (see moe_ffn_forward_host); the device
         scratch is kept on the layer (grown on demand, zeroed when made)."""
-        import torch
         T = x.shape[0]
         nbytes = moe_ffn_host_scratch_bytes(self.handle, T)
         if nbytes == 0:
             raise RfxError(-2, f"unsupported T={T}")
-        if getattr(self, "host_scratch", None) is None or self.host_scratch.numel() < nbytes:
-            self.host_scratch = torch.empty(nbytes, dtype=torch.uint8, device=self.ws.device)
-            rfx_ws_init(self.host_scratch, stream)
-        moe_ffn_forward_host(self.handle, x, logits, T, y, self.host_scratch, stream)
+        stream = _stream(stream)
+        moe_ffn_forward_host(self.handle, x, logits, T, y, self._kept("host_scratch", nbytes, stream), stream)
 
     def host_status(self, stream=None) -> int:
         """Device flag of the host-call scratch (its workspace comes first)."""
@@ -699,19 +713,17 @@ class MoeLayer:
     def prefill(self, x, idx, w, y, stream=None, exact=False):
         """moe_ffn_prefill (exact: moe_ffn_prefill_ex at RFX_PREFILL_EXACT) with a
         workspace kept on the layer (grown on demand)."""
-        import torch
         T = x.shape[0]
         prec = RFX_PREFILL_EXACT if exact else RFX_PREFILL_BF16
         nbytes = moe_prefill_workspace_bytes_ex(self.handle, T, prec)
         if nbytes == 0:
             raise RfxError(-2, f"prefill unsupported for T={T}, H={self.H}, I={self.I}")
-        if getattr(self, "pf_ws", None) is None or self.pf_ws.numel() < nbytes:
-            self.pf_ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-            rfx_ws_init(self.pf_ws)
+        stream = _stream(stream)
+        ws = self._kept("pf_ws", nbytes, stream)
         if exact:
-            moe_ffn_prefill_ex(self.handle, x, T, idx, w, y, self.pf_ws, prec, stream)
+            moe_ffn_prefill_ex(self.handle, x, T, idx, w, y, ws, prec, stream)
         else:
-            moe_ffn_prefill(self.handle, x, T, idx, w, y, self.pf_ws, stream)
+            moe_ffn_prefill(self.handle, x, T, idx, w, y, ws, stream)
 
     def prefill_view(self, T: int):
         return moe_prefill_view(self.handle, T, self.pf_ws, self.I, self.E)

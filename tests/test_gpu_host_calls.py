@@ -186,3 +186,91 @@ def test_uploads_run_ahead_unless_the_scratch_itself_was_zeroed(part):
     torch.cuda.synchronize()
     assert seen == (part is None)
     check(ml, x, logits, y)
+
+
+def device_inputs(T, seed):
+    x, logits, _ = host_inputs(T, seed)
+    idx = torch.empty((T, K), dtype=torch.int32, device=DEV)
+    w = torch.empty((T, K), device=DEV)
+    rfx.moe_router_topk(logits.to(DEV), K, idx, w)
+    return x.to(DEV), idx, w
+
+
+def test_a_kept_workspace_is_made_on_the_stream_of_its_call():
+    """MoeLayer's own workspaces on a side stream while the current one is busy: neither the zeroing nor what the
+    current stream still has to write to memory that torch gave back may fall into the call."""
+    _, (ml,) = layers(1)
+    T = 40
+    x, idx, w = device_inputs(T, 5)
+    want, y = torch.empty((T, H), device=DEV), torch.empty((T, H), device=DEV)
+    ml.prefill(x, idx, w, want)
+    counts = ml.prefill_view(T)["counts"].clone()
+    _, (ml,) = layers(1)
+    hx, hl, hy = host_inputs(T, 6)
+    side = torch.cuda.Stream()
+    n = max(rfx.moe_prefill_workspace_bytes(ml.handle, T), rfx.moe_ffn_host_scratch_bytes(ml.handle, T))
+    old = [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    for t in old:
+        t.fill_(0xFF)
+    del old, t
+    ml.prefill(x, idx, w, y, stream=side)
+    ml.forward_host(hx, hl, hy, stream=side)
+    side.synchronize()
+    first = hy.clone()
+    hy.fill_(float("nan"))
+    torch.cuda.synchronize()
+    assert torch.equal(ml.prefill_view(T)["counts"], counts)
+    torch.testing.assert_close(y, want, rtol=1e-5, atol=1e-5 * float(want.abs().max()))
+    ml.forward_host(hx, hl, hy, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert ml.host_status() == rfx.RFX_OK and ml.prefill_status() == rfx.RFX_OK
+    check(ml, hx, hl, first)
+    check(ml, hx, hl, hy)
+
+
+def test_a_grown_workspace_does_not_take_the_old_one_from_its_stream():
+    # the old scratch goes back to torch while a side stream's call still works in it
+    _, (ml,) = layers(1)
+    small, big = host_inputs(8, 21), host_inputs(300, 22)
+    n = rfx.moe_ffn_host_scratch_bytes(ml.handle, 8)
+    ml.forward_host(*host_inputs(8, 20))             # the scratch comes from the current stream ...
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    ml.forward_host(*small, stream=side)             # ... is used on the other ...
+    ml.forward_host(*big, stream=side)               # ... and outgrown
+    for _ in range(8):
+        torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0xFF)
+    torch.cuda.synchronize()
+    assert ml.host_status() == rfx.RFX_OK
+    check(ml, *small)
+    check(ml, *big)
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_kept_workspaces_in_a_captured_call(T):
+    _, (ml,) = layers(1)
+    hx, hl, hy = host_inputs(T, 31)
+    x, idx, w = device_inputs(T, 32)
+    y, want = torch.empty((T, H), device=DEV), torch.empty((T, H), device=DEV)
+    ml.forward_host(hx, hl, hy)
+    ml.prefill(x, idx, w, want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ml.forward_host(hx, hl, hy)
+        ml.prefill(x, idx, w, y)
+    new = host_inputs(T, 33)
+    hx.copy_(new[0])
+    hl.copy_(new[1])
+    hy.fill_(float("nan"))
+    y.fill_(float("nan"))
+    graph.replay()
+    ml.forward_host(*new)
+    torch.cuda.synchronize()
+    check(ml, hx, hl, hy)
+    check(ml, *new)
+    torch.testing.assert_close(y, want, rtol=1e-5, atol=1e-5 * float(want.abs().max()))
