@@ -671,15 +671,19 @@ class MoeLayer:
         """The workspace kept as `name`, grown to nbytes, for a call on `stream`: its memory comes from that
         stream and is zeroed there, and goes back when every stream that used it is through."""
         import torch
-        ws = getattr(self, name, None)
+        dev, ws = self.ws.device, getattr(self, name, None)
+
+        def known():   # 0 to 2: the default streams, which wait for one another
+            return torch.cuda.default_stream(dev) if stream <= 2 else torch.cuda.ExternalStream(stream, device=dev)
+
         if ws is None or ws.numel() < nbytes:
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.ws.device)):
-                ws = torch.empty(nbytes, dtype=torch.uint8, device=self.ws.device)
+            with torch.cuda.stream(known()):
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
             rfx_ws_init(ws, stream)
             setattr(self, name, ws)
             self._used_on[name] = {stream}
         elif stream not in self._used_on[name]:
-            ws.record_stream(torch.cuda.ExternalStream(stream, device=ws.device))
+            ws.record_stream(known())
             self._used_on[name].add(stream)
         return ws
 

@@ -488,8 +488,10 @@ int moe_ffn_forward_logits(const moe_layer* layer, const void* x, int T, const f
  * copies to be asynchronous).  The two uploads run on a stream the layer
  * makes on first use, into one of two buffer sets used in turn, and `stream`
  * waits for them: a call's uploads overlap the kernels of the call before
- * it, where the scratch's last call was the same layer's with the same T.  Otherwise (another T, another
- * layer, a scratch that a captured call uses too) they wait for what `stream` holds at the call.  The kernels and the download run on `stream`; x, the logits and y may
+ * it, where the scratch's last call was the same layer's with the same T.
+ * Otherwise (another T, another layer, a scratch that a captured call uses
+ * too) they wait for what `stream` holds at the call.  The kernels and the
+ * download run on `stream`; x, the logits and y may
  * be reused once `stream` has synchronised.  For T <= 8 a y in page-locked
  * host memory that the device can address (cudaHostAlloc, cudaHostRegister)
  * receives the decode kernel's stores directly instead of a copy.  Inside a CUDA graph capture

@@ -274,3 +274,16 @@ def test_kept_workspaces_in_a_captured_call(T):
     check(ml, hx, hl, hy)
     check(ml, *new)
     torch.testing.assert_close(y, want, rtol=1e-5, atol=1e-5 * float(want.abs().max()))
+
+
+@pytest.mark.parametrize("stream", [0, 1, 2])
+def test_kept_workspaces_on_the_default_streams(stream):
+    # the handles of the legacy and the per-thread default stream
+    _, (ml,) = layers(1)
+    for T in (2, 40, 2):
+        x, logits, y = host_inputs(T, 50 + T)
+        torch.cuda.synchronize()
+        ml.forward_host(x, logits, y, stream=stream)
+        torch.cuda.synchronize()
+        check(ml, x, logits, y)
+    assert ml.host_status() == rfx.RFX_OK
